@@ -43,7 +43,10 @@ EXPORTS = ("moe_check_config", "moe_workspace_size", "moe_status_string", "moe_l
            "moe_ep_fanout_fp8", "moe_ep_combine_plan", "moe_ep_dispatch_dedup_plan",
            "moe_ep_precombine", "moe_ep_combine_dedup", "moe_ipc_get_handle",
            "moe_ipc_open_handle", "moe_ipc_close_handle", "moe_packed_weights_size",
-           "moe_pack_weights", "moe_expert_ffn_packed", "moe_forward_packed")
+           "moe_pack_weights", "moe_expert_ffn_packed", "moe_forward_packed",
+           "moe_balance_loss", "moe_route_backward", "moe_combine_backward",
+           "moe_int8_workspace_size", "moe_quantize_weights_int8", "moe_dispatch_int8",
+           "moe_expert_ffn_int8", "moe_forward_int8")
 
 MOE_ROUTER_SIGMOID, MOE_ROUTER_SQRT_SOFTPLUS, MOE_ROUTER_HASH = 0, 1, 2
 MOE_PAYLOAD_BF16, MOE_PAYLOAD_FP8 = 0, 1
@@ -69,6 +72,48 @@ class MoeConfig(C.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class Int8Weights(C.Structure):
+    """Mirror of ``moe_int8_weights`` that keeps the tensors it points to.
+
+    ``Int8Weights(w_gate=..., w_gate_scale=..., ...)`` takes int8 codes and fp32 scales of the
+    header's layouts (the ``ws_`` ones only for a layer with shared experts); they become
+    attributes of ``tensors``.  ``quantize_weights_int8`` makes one from bf16 weights.
+    """
+    _codes = ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")
+    _fields_ = [(n, C.c_void_p) for n in _codes] + [(n + "_scale", C.c_void_p) for n in _codes]
+
+    def __init__(self, **tensors):
+        names = {n for n, _ in self._fields_}
+        for n, t in tensors.items():
+            if n not in names:
+                raise TypeError(f"Int8Weights: no field {n!r}")
+            if t is not None and (t.dtype != (torch.int8 if n in self._codes else torch.float32)
+                                  or not t.is_contiguous()):
+                raise TypeError(f"Int8Weights: {n} must be a contiguous tensor of int8 codes or "
+                                "fp32 scales")
+        super().__init__(**{n: None if t is None else t.data_ptr() for n, t in tensors.items()})
+        self.tensors = dict(tensors)
+
+    def check(self, fn, c):
+        """Raises MoeError unless every tensor given has the size of configuration ``c`` and lies
+        on the current GPU.  A passed configuration is remembered: the tensors never change."""
+        if not all(t is None or t.is_cuda for t in self.tensors.values()):
+            raise MoeError(fn, MOE_ERR_INVALID_ARG)
+        key = (c.d, c.E, c.d_ff, c.n_shared, c.d_ff_shared,
+               torch.cuda.current_device() if self.tensors else None)
+        if key == self.__dict__.get("_checked"):
+            return
+        up, up_s = c.d_ff, c.n_shared * c.d_ff_shared
+        sizes = {"w_gate": c.E * up * c.d, "w_up": c.E * up * c.d, "w_down": c.E * up * c.d,
+                 "w_gate_scale": c.E * up, "w_up_scale": c.E * up, "w_down_scale": c.E * c.d,
+                 "ws_gate": up_s * c.d, "ws_up": up_s * c.d, "ws_down": up_s * c.d,
+                 "ws_gate_scale": up_s, "ws_up_scale": up_s, "ws_down_scale": c.d}
+        for n, t in self.tensors.items():
+            if t is not None and (c.n_shared > 0 or not n.startswith("ws_")):
+                _tensor(fn, t, t.dtype, sizes[n])
+        self._checked = key
 
 
 class MoeError(RuntimeError):
@@ -132,6 +177,18 @@ _sig = {
     "moe_forward_packed": (C.c_int, [_CP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                      _P, _S, _P]),
 }
+_WP = C.POINTER(Int8Weights)
+_F32, _I32 = C.c_float, C.c_int32
+_sig |= {
+    "moe_balance_loss": (C.c_int, [_CP, _P, _P, _P, _I32, _F32, _P, _P, _P, _P, _S, _P]),
+    "moe_route_backward": (C.c_int, [_CP, _P, _P, _P, _P, _I32, _P, _P, _F32, _P, _P, _P]),
+    "moe_combine_backward": (C.c_int, [_CP] + [_P] * 7),
+    "moe_int8_workspace_size": (_S, [_CP]),
+    "moe_quantize_weights_int8": (C.c_int, [_CP] + [_P] * 6 + [_WP, _P]),
+    "moe_dispatch_int8": (C.c_int, [_CP] + [_P] * 11 + [_S, _P]),
+    "moe_expert_ffn_int8": (C.c_int, [_CP, _P, _P, _P, _WP, _P, _P, _P, _P, _S, _P]),
+    "moe_forward_int8": (C.c_int, [_CP] + [_P] * 5 + [_WP] + [_P] * 8 + [_S, _P]),
+}
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
     _f.restype, _f.argtypes = _res, _args
@@ -164,6 +221,30 @@ def _ok(fn, st):
 
 def _ws(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _config(cfg):
+    return cfg if isinstance(cfg, MoeConfig) else MoeConfig.of(cfg)
+
+
+def _tensor(fn, t, dtype, numel):
+    """The device pointer of a tensor argument after checking it: dtype, contiguous, at least
+    ``numel`` elements, on the current GPU.  None and raw device pointers pass as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    if (t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel or not t.is_cuda
+            or t.get_device() != torch.cuda.current_device()):
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return t.data_ptr()
+
+
+def _sequences(fn, seq_offsets):
+    """(device pointer, number of sequences) of a seq_offsets argument."""
+    if seq_offsets is None:
+        return None, 1
+    if seq_offsets.numel() < 1:
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return _tensor(fn, seq_offsets, torch.int32, 1), seq_offsets.numel() - 1
 
 
 # ----------------------------------------------------------------- queries
@@ -263,6 +344,140 @@ def moe_expert_ffn_gather(cfg, x, perm_token, offsets, w_gate, w_up, w_down, y_p
 def moe_permute(cfg, x, inv_perm, x_perm, stream=None) -> None:
     _ok("moe_permute", _lib.moe_permute(_cfg(cfg), _ptr(x), _ptr(inv_perm), _ptr(x_perm),
                                         _stream(stream)))
+
+
+# ----------------------------------------------------------------- the router's training side
+def moe_balance_loss(cfg, scores, topk_idx, seq_offsets, alpha, counts, prob, loss, ws,
+                     stream=None) -> None:
+    """Per-sequence balance loss, counts and mean affinities (seq_offsets None: one sequence)."""
+    c, fn = _config(cfg), "moe_balance_loss"
+    seq, n = _sequences(fn, seq_offsets)
+    wp, wn = _ws(ws)
+    _ok(fn, _lib.moe_balance_loss(
+        C.byref(c), _tensor(fn, scores, torch.float32, c.T * c.E),
+        _tensor(fn, topk_idx, torch.int32, c.T * c.K), seq, n, alpha,
+        _tensor(fn, counts, torch.int32, n * c.E), _tensor(fn, prob, torch.float32, n * c.E),
+        _tensor(fn, loss, torch.float32, n), wp, wn, _stream(stream)))
+
+
+def moe_route_backward(cfg, scores, topk_idx, d_topk_w, seq_offsets, counts, d_loss, alpha,
+                       d_logits, device_status=None, stream=None) -> None:
+    """Gradient of the gates (d_topk_w, or None) and of the balance loss (d_loss, or None) with
+    respect to the router's logits."""
+    c, fn = _config(cfg), "moe_route_backward"
+    seq, n = _sequences(fn, seq_offsets) if d_loss is not None else (None, 1)
+    _ok(fn, _lib.moe_route_backward(
+        C.byref(c), _tensor(fn, scores, torch.float32, c.T * c.E),
+        _tensor(fn, topk_idx, torch.int32, c.T * c.K),
+        _tensor(fn, d_topk_w, torch.float32, c.T * c.K), seq, n,
+        _tensor(fn, counts, torch.int32, n * c.E), _tensor(fn, d_loss, torch.float32, n), alpha,
+        _tensor(fn, d_logits, torch.float32, c.T * c.E),
+        _tensor(fn, device_status, torch.int32, 1), _stream(stream)))
+
+
+def moe_combine_backward(cfg, d_out, y_perm, inv_perm, topk_w, d_y_perm, d_topk_w,
+                         stream=None) -> None:
+    c, fn = _config(cfg), "moe_combine_backward"
+    rows = c.T * c.K
+    _ok(fn, _lib.moe_combine_backward(
+        C.byref(c), _tensor(fn, d_out, torch.bfloat16, c.T * c.d),
+        _tensor(fn, y_perm, torch.bfloat16, rows * c.d), _tensor(fn, inv_perm, torch.int32, rows),
+        _tensor(fn, topk_w, torch.float32, rows),
+        _tensor(fn, d_y_perm, torch.bfloat16, rows * c.d),
+        _tensor(fn, d_topk_w, torch.float32, rows), _stream(stream)))
+
+
+# ----------------------------------------------------------------- experts in int8
+def moe_int8_workspace_size(cfg) -> int:
+    return _lib.moe_int8_workspace_size(_cfg(cfg))
+
+
+def alloc_int8_workspace(cfg, device="cuda") -> torch.Tensor:
+    """Device workspace of moe_int8_workspace_size(cfg) bytes; serves every entry point."""
+    n = moe_int8_workspace_size(cfg)
+    if n == 0:
+        raise MoeError("moe_int8_workspace_size",
+                       moe_check_config(cfg) or MOE_ERR_UNSUPPORTED_SHAPE)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, weights,
+                              stream=None) -> None:
+    c, fn = _config(cfg), "moe_quantize_weights_int8"
+    weights.check(fn, c)
+    n, ns = c.E * c.d_ff * c.d, c.n_shared * c.d_ff_shared * c.d
+    ptrs = [_tensor(fn, t, torch.bfloat16, n) for t in (w_gate, w_up, w_down)]
+    ptrs += [_tensor(fn, t, torch.bfloat16, ns) for t in (ws_gate, ws_up, ws_down)]
+    _ok(fn, _lib.moe_quantize_weights_int8(C.byref(c), *ptrs, C.byref(weights), _stream(stream)))
+
+
+def quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None,
+                          stream=None) -> Int8Weights:
+    """Allocates codes and scales for the bf16 weights and fills them with
+    moe_quantize_weights_int8.  (On a stream that is not the current one, the caller orders the
+    allocation before it.)"""
+    c = _config(cfg)
+    dev = w_gate.device
+    ns, ffs = c.n_shared, c.d_ff_shared
+    shapes = {"w_gate": (c.E, c.d_ff, c.d), "w_up": (c.E, c.d_ff, c.d), "w_down": (c.E, c.d, c.d_ff)}
+    scales = {"w_gate": (c.E, c.d_ff), "w_up": (c.E, c.d_ff), "w_down": (c.E, c.d)}
+    if ns > 0:
+        shapes |= {"ws_gate": (ns, ffs, c.d), "ws_up": (ns, ffs, c.d), "ws_down": (ns, c.d, ffs)}
+        scales |= {"ws_gate": (ns, ffs), "ws_up": (ns, ffs), "ws_down": (c.d,)}
+    t = {n: torch.empty(s, dtype=torch.int8, device=dev) for n, s in shapes.items()}
+    t |= {n + "_scale": torch.empty(s, dtype=torch.float32, device=dev) for n, s in scales.items()}
+    w = Int8Weights(**t)
+    moe_quantize_weights_int8(c, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, w, stream)
+    return w
+
+
+def moe_dispatch_int8(cfg, x, topk_idx, counts, offsets, send, send_tok, perm_token, inv_perm,
+                      x_perm_q, x_scale, ws, stream=None) -> None:
+    c, fn = _config(cfg), "moe_dispatch_int8"
+    wp, wn = _ws(ws)
+    rows, i32 = c.T * c.K, torch.int32
+    _ok(fn, _lib.moe_dispatch_int8(
+        C.byref(c), _tensor(fn, x, torch.bfloat16, c.T * c.d), _tensor(fn, topk_idx, i32, rows),
+        _tensor(fn, counts, i32, c.E), _tensor(fn, offsets, i32, c.E + 1),
+        _tensor(fn, send, i32, c.G * c.G), _tensor(fn, send_tok, i32, c.G * c.G),
+        _tensor(fn, perm_token, i32, rows), _tensor(fn, inv_perm, i32, rows),
+        _tensor(fn, x_perm_q, torch.int8, rows * c.d), _tensor(fn, x_scale, torch.float32, rows),
+        wp, wn, _stream(stream)))
+
+
+def moe_expert_ffn_int8(cfg, x_perm_q, x_scale, offsets, weights, y_perm, x, y_shared, ws,
+                        stream=None) -> None:
+    """weights: Int8Weights."""
+    c, fn = _config(cfg), "moe_expert_ffn_int8"
+    wp, wn = _ws(ws)
+    rows = c.T * c.K
+    weights.check(fn, c)
+    _ok(fn, _lib.moe_expert_ffn_int8(
+        C.byref(c), _tensor(fn, x_perm_q, torch.int8, rows * c.d),
+        _tensor(fn, x_scale, torch.float32, rows), _tensor(fn, offsets, torch.int32, c.E + 1),
+        C.byref(weights), _tensor(fn, y_perm, torch.bfloat16, rows * c.d),
+        _tensor(fn, x, torch.bfloat16, c.T * c.d),
+        _tensor(fn, y_shared, torch.bfloat16, c.T * c.d), wp, wn, _stream(stream)))
+
+
+def moe_forward_int8(cfg, x, router_w, logit_offset, bias, weights, out, topk_idx=None,
+                     topk_w=None, counts=None, offsets=None, send=None, send_tok=None, ws=None,
+                     stream=None, token_ids=None) -> None:
+    """weights: Int8Weights; ws: alloc_int8_workspace(cfg)."""
+    c, fn = _config(cfg), "moe_forward_int8"
+    wp, wn = _ws(ws)
+    rows, i32, f32 = c.T * c.K, torch.int32, torch.float32
+    weights.check(fn, c)
+    _ok(fn, _lib.moe_forward_int8(
+        C.byref(c), _tensor(fn, x, torch.bfloat16, c.T * c.d),
+        _tensor(fn, router_w, f32, c.E * c.d), _tensor(fn, logit_offset, f32, c.E),
+        _tensor(fn, bias, f32, c.E), _tensor(fn, token_ids, torch.int64, c.T), C.byref(weights),
+        _tensor(fn, out, torch.bfloat16, c.T * c.d), _tensor(fn, topk_idx, i32, rows),
+        _tensor(fn, topk_w, f32, rows), _tensor(fn, counts, i32, c.E),
+        _tensor(fn, offsets, i32, c.E + 1), _tensor(fn, send, i32, c.G * c.G),
+        _tensor(fn, send_tok, i32, c.G * c.G), wp, wn, _stream(stream)))
 
 
 # ----------------------------------------------------------------- expert parallelism

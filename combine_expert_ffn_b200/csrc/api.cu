@@ -85,6 +85,32 @@ Layout layout(const moe_config &c) {
     return L;
 }
 
+// The int8 workspace: layout() and, behind it, what the int8 experts need
+// besides.  The codes of h lie in the region of the bf16 h, with their scales
+// behind them (d_ff + 4 <= 2 d_ff bytes a row), the payload in that of x_perm.
+struct Int8Layout {
+    Layout base;
+    size_t h, h_sh, x_q, x_q_scale, total;
+};
+
+Int8Layout int8_layout(const moe_config &c) {
+    Int8Layout L{};
+    L.base = layout(c);
+    size_t off = L.base.total;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes, 256);
+        return at;
+    };
+    const size_t T = (size_t)c.T, ffs = (size_t)c.n_shared * (size_t)c.d_ff_shared;
+    L.h = take(4 * T * (size_t)c.K * (size_t)c.d_ff);
+    L.h_sh = take(4 * T * ffs);
+    L.x_q = take(c.n_shared > 0 ? T * (size_t)c.d : 0);
+    L.x_q_scale = take(c.n_shared > 0 ? 4 * T : 0);
+    L.total = off;
+    return L;
+}
+
 template <typename T>
 T *at(void *ws, size_t off) {
     return reinterpret_cast<T *>(static_cast<char *>(ws) + off);
@@ -293,6 +319,56 @@ moe_status moe_bias_update(const moe_config *c, const int32_t *counts, float gam
     return cuda_status(launch_bias_update(counts, c->E, c->T, c->K, gamma, bias, as_stream(stream)));
 }
 
+moe_status moe_balance_loss(const moe_config *c, const float *scores, const int32_t *topk_idx,
+                            const int32_t *seq_offsets, int32_t n_seq, float alpha,
+                            int32_t *counts, float *prob, float *loss, void *ws, size_t ws_bytes,
+                            void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (n_seq < 0 || (!seq_offsets && n_seq != 1) || !ws) return MOE_ERR_INVALID_ARG;
+    if (!(alpha - alpha == 0.0f)) return MOE_ERR_INVALID_ARG;  // finite
+    if (n_seq > 0 && (!counts || !prob || !loss)) return MOE_ERR_INVALID_ARG;
+    if (c->T > 0 && (!scores || !topk_idx)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(scores)) return MOE_ERR_INVALID_ARG;
+    const Layout L = layout(*c);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    if ((st = check_device())) return st;
+    StageRange range("moe.balance_loss");
+    // the tiles' shares ([tiles, 2, E] floats and as many counts) fit the region of
+    // the affinities: where there are two tiles or more, T >= 4 * tiles
+    const int tile = balance_tile(c->T);
+    const int tiles = (int)(((int64_t)c->T + tile - 1) / tile);
+    float *part = at<float>(ws, L.scores);
+    int32_t *part_n = reinterpret_cast<int32_t *>(part + (size_t)tiles * 2 * c->E);
+    return cuda_status(launch_balance_loss(scores, topk_idx, seq_offsets, n_seq, alpha, c->T, c->E,
+                                           c->K, counts, prob, loss, part, part_n,
+                                           at<int32_t>(ws, L.status), as_stream(stream)));
+}
+
+moe_status moe_route_backward(const moe_config *c, const float *scores, const int32_t *topk_idx,
+                              const float *d_topk_w, const int32_t *seq_offsets, int32_t n_seq,
+                              const int32_t *counts, const float *d_loss, float alpha,
+                              float *d_logits, int32_t *device_status, void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (c->router == MOE_ROUTER_HASH) return MOE_ERR_INVALID_ARG;
+    if (!d_topk_w && !d_loss) return MOE_ERR_INVALID_ARG;
+    if (d_loss) {
+        if (n_seq < 0 || (!seq_offsets && n_seq != 1)) return MOE_ERR_INVALID_ARG;
+        if (n_seq > 0 && !counts) return MOE_ERR_INVALID_ARG;
+        if (!(alpha - alpha == 0.0f)) return MOE_ERR_INVALID_ARG;  // finite
+    }
+    if (c->T > 0 && (!scores || !d_logits || (d_topk_w && !topk_idx))) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(scores) || !aligned16(d_logits)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_device())) return st;
+    StageRange range("moe.route_backward");
+    return cuda_status(launch_route_backward(scores, topk_idx, d_topk_w, seq_offsets, n_seq, counts,
+                                             d_loss, alpha, c->T, c->E, c->K,
+                                             c->router == MOE_ROUTER_SQRT_SOFTPLUS, d_logits,
+                                             device_status, as_stream(stream)));
+}
+
 moe_status moe_dispatch(const moe_config *c, const void *x, const int32_t *topk_idx,
                         int32_t *counts, int32_t *offsets, int32_t *send, int32_t *send_tok,
                         int32_t *perm_token, int32_t *inv_perm, void *x_perm, void *ws,
@@ -451,6 +527,24 @@ moe_status moe_expert_ffn_gather(const moe_config *c, const void *x, const int32
     a.status = at<int32_t>(ws, L.status);
     a.timeout_ns = kWaitTimeoutNs;
     return cuda_status(launch_expert_ffn(a, as_stream(stream)));
+}
+
+moe_status moe_combine_backward(const moe_config *c, const void *d_out, const void *y_perm,
+                                const int32_t *inv_perm, const float *topk_w, void *d_y_perm,
+                                float *d_topk_w, void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (!d_y_perm && !d_topk_w) return MOE_ERR_INVALID_ARG;
+    if (c->T > 0) {
+        if (!d_out || !inv_perm) return MOE_ERR_INVALID_ARG;
+        if ((d_y_perm && !topk_w) || (d_topk_w && !y_perm)) return MOE_ERR_INVALID_ARG;
+    }
+    if (!aligned16(d_out) || !aligned16(y_perm) || !aligned16(d_y_perm)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_device())) return st;
+    StageRange range("moe.combine_backward");
+    return cuda_status(launch_combine_backward(d_out, y_perm, inv_perm, topk_w, c->T, c->d, c->K,
+                                               (int64_t)c->T * c->K, d_y_perm, d_topk_w,
+                                               as_stream(stream)));
 }
 
 moe_status moe_combine(const moe_config *c, const void *y_perm, const int32_t *inv_perm,
@@ -1030,6 +1124,208 @@ moe_status moe_selftest_bounded_wait(int64_t timeout_ns, void *ws, void *stream)
     if (st) return st;
     return cuda_status(launch_bounded_wait_selftest(timeout_ns, static_cast<int32_t *>(ws),
                                                     as_stream(stream)));
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------- int8 experts
+namespace {
+// the exact 32-bit sums: a reduction over n codes stays within 2^14 n < 2^31
+bool int8_lengths_ok(const moe_config &c) {
+    return c.d < 131072 && c.d_ff < 131072 && (int64_t)c.n_shared * c.d_ff_shared < 131072;
+}
+
+moe_status check_int8_weights(const moe_config &c, const moe_int8_weights *w) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    const void *routed[] = {w->w_gate, w->w_up, w->w_down, w->w_gate_scale, w->w_up_scale,
+                            w->w_down_scale};
+    const void *shared[] = {w->ws_gate, w->ws_up, w->ws_down, w->ws_gate_scale, w->ws_up_scale,
+                            w->ws_down_scale};
+    for (const void *p : routed)
+        if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    for (const void *p : shared)
+        if (c.n_shared > 0 && (!p || !aligned16(p))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+cudaError_t ffn_int8(const moe_config &c, const int8_t *x_perm_q, const float *x_scale,
+                     const int32_t *offsets, const moe_int8_weights &w, void *y_perm,
+                     void *y_shared, void *ws, const Int8Layout &L, cudaStream_t s) {
+    const size_t rows = (size_t)c.T * c.K, ffs = (size_t)c.n_shared * c.d_ff_shared;
+    FfnInt8Args a{};
+    a.T = c.T; a.d = c.d; a.E = c.E; a.K = c.K; a.d_ff = c.d_ff;
+    a.n_shared = c.n_shared; a.d_ff_shared = c.d_ff_shared;
+    a.x_perm_q = x_perm_q; a.x_scale = x_scale; a.offsets = offsets; a.w = w;
+    a.h = at<float>(ws, L.h);
+    a.h_q = at<int8_t>(ws, L.base.h);
+    a.h_scale = at<float>(ws, L.base.h + rows * c.d_ff);
+    a.y_perm = y_perm;
+    a.x_q = at<int8_t>(ws, L.x_q);
+    a.x_q_scale = at<float>(ws, L.x_q_scale);
+    a.h_shared = at<float>(ws, L.h_sh);
+    a.h_shared_q = at<int8_t>(ws, L.base.h_sh);
+    a.h_shared_scale = at<float>(ws, L.base.h_sh + (size_t)c.T * ffs);
+    a.y_shared = y_shared;
+    a.status = at<int32_t>(ws, L.base.status);
+    a.timeout_ns = kWaitTimeoutNs;
+    return launch_expert_ffn_int8(a, s);
+}
+}  // namespace
+
+extern "C" {
+
+size_t moe_int8_workspace_size(const moe_config *c) {
+    if (moe_check_config(c) != MOE_OK || !int8_lengths_ok(*c)) return 0;
+    return int8_layout(*c).total;
+}
+
+moe_status moe_quantize_weights_int8(const moe_config *c, const void *w_gate, const void *w_up,
+                                     const void *w_down, const void *ws_gate, const void *ws_up,
+                                     const void *ws_down, const moe_int8_weights *out,
+                                     void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (!int8_lengths_ok(*c)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!w_gate || !w_up || !w_down) return MOE_ERR_INVALID_ARG;
+    if (c->n_shared > 0 && (!ws_gate || !ws_up || !ws_down)) return MOE_ERR_INVALID_ARG;
+    const void *ptrs[] = {w_gate, w_up, w_down, ws_gate, ws_up, ws_down};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if ((st = check_int8_weights(*c, out))) return st;
+    if ((st = check_device())) return st;
+    cudaStream_t s = as_stream(stream);
+    const int64_t up_rows = (int64_t)c->E * c->d_ff, down_rows = (int64_t)c->E * c->d;
+    if (launch_quantize_rows_bf16(w_gate, up_rows, c->d, out->w_gate, out->w_gate_scale, s) ||
+        launch_quantize_rows_bf16(w_up, up_rows, c->d, out->w_up, out->w_up_scale, s) ||
+        launch_quantize_rows_bf16(w_down, down_rows, c->d_ff, out->w_down, out->w_down_scale, s))
+        return MOE_ERR_CUDA;
+    if (c->n_shared == 0) return MOE_OK;
+    const int64_t sh_rows = (int64_t)c->n_shared * c->d_ff_shared;
+    if (launch_quantize_rows_bf16(ws_gate, sh_rows, c->d, out->ws_gate, out->ws_gate_scale, s) ||
+        launch_quantize_rows_bf16(ws_up, sh_rows, c->d, out->ws_up, out->ws_up_scale, s))
+        return MOE_ERR_CUDA;
+    return cuda_status(launch_quantize_joint_bf16(ws_down, c->n_shared, c->d, c->d_ff_shared,
+                                                  out->ws_down, out->ws_down_scale, s));
+}
+
+moe_status moe_dispatch_int8(const moe_config *c, const void *x, const int32_t *topk_idx,
+                             int32_t *counts, int32_t *offsets, int32_t *send, int32_t *send_tok,
+                             int32_t *perm_token, int32_t *inv_perm, int8_t *x_perm_q,
+                             float *x_scale, void *ws, size_t ws_bytes, void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (!counts || !offsets || !send || !ws) return MOE_ERR_INVALID_ARG;
+    if (c->T > 0 && (!x || !topk_idx || !perm_token || !inv_perm || !x_perm_q || !x_scale))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(x_perm_q) || !aligned16(x_scale)) return MOE_ERR_INVALID_ARG;
+    const Layout L = layout(*c);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    if ((st = check_device())) return st;
+    StageRange range("moe.dispatch");
+    cudaStream_t s = as_stream(stream);
+    DispatchWs dw{at<int32_t>(ws, L.hist_t), at<int32_t>(ws, L.base_t),
+                  at<int32_t>(ws, L.send_part), at<int32_t>(ws, L.sendtok_part)};
+    if (launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send, send_tok,
+                        perm_token, inv_perm, nullptr, dw, at<int32_t>(ws, L.status), s))
+        return MOE_ERR_CUDA;
+    return cuda_status(launch_gather_int8(x, inv_perm, c->T, c->d, c->K, x_perm_q, x_scale, nullptr,
+                                          nullptr, s));
+}
+
+moe_status moe_expert_ffn_int8(const moe_config *c, const int8_t *x_perm_q, const float *x_scale,
+                               const int32_t *offsets, const moe_int8_weights *w, void *y_perm,
+                               const void *x, void *y_shared, void *ws, size_t ws_bytes,
+                               void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (!int8_lengths_ok(*c)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!ws) return MOE_ERR_INVALID_ARG;
+    if (c->T > 0) {
+        if (!x_perm_q || !x_scale || !offsets || !y_perm) return MOE_ERR_INVALID_ARG;
+        if (c->n_shared > 0 && (!x || !y_shared)) return MOE_ERR_INVALID_ARG;
+        if ((st = check_int8_weights(*c, w))) return st;
+    }
+    const void *ptrs[] = {x_perm_q, x_scale, y_perm, x, y_shared};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    const Int8Layout L = int8_layout(*c);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    if ((st = check_device())) return st;
+    if (c->T == 0) return MOE_OK;
+    StageRange range("moe.expert_ffn");
+    cudaStream_t s = as_stream(stream);
+    if (c->n_shared > 0 &&
+        launch_quantize_rows_bf16(x, c->T, c->d, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_q_scale),
+                                  s))
+        return MOE_ERR_CUDA;
+    return cuda_status(ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_shared, ws, L, s));
+}
+
+moe_status moe_forward_int8(const moe_config *c, const void *x, const float *router_w,
+                            const float *logit_offset, const float *bias,
+                            const int64_t *token_ids, const moe_int8_weights *w, void *out,
+                            int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets,
+                            int32_t *send, int32_t *send_tok, void *ws, size_t ws_bytes,
+                            void *stream) {
+    moe_status st = moe_check_config(c);
+    if (st) return st;
+    if (c->payload != MOE_PAYLOAD_BF16 || !int8_lengths_ok(*c)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!ws) return MOE_ERR_INVALID_ARG;
+    if (c->T > 0) {
+        if (!x || !out) return MOE_ERR_INVALID_ARG;
+        if (c->router != MOE_ROUTER_HASH && !router_w) return MOE_ERR_INVALID_ARG;
+        if ((st = check_int8_weights(*c, w))) return st;
+    }
+    if (!aligned16(x) || !aligned16(router_w) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+    const Int8Layout L8 = int8_layout(*c);
+    const Layout &L = L8.base;
+    if (ws_bytes < L8.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    if ((st = check_device())) return st;
+    if (c->T == 0) return MOE_OK;
+
+    cudaStream_t s = as_stream(stream);
+    if (!topk_idx) topk_idx = at<int32_t>(ws, L.topk_idx);
+    if (!topk_w) topk_w = at<float>(ws, L.topk_w);
+    if (!counts) counts = at<int32_t>(ws, L.counts);
+    if (!offsets) offsets = at<int32_t>(ws, L.offsets);
+    if (!send) send = at<int32_t>(ws, L.send);
+    if (!send_tok) send_tok = at<int32_t>(ws, L.send_tok);
+    int32_t *perm_token = at<int32_t>(ws, L.perm_token);
+    int32_t *inv_perm = at<int32_t>(ws, L.inv_perm);
+    void *y_perm = at<void>(ws, L.y_perm);
+    void *y_sh = c->n_shared > 0 ? at<void>(ws, L.y_sh) : nullptr;
+
+    StageRange layer("moe.forward");
+    StageRange stage("moe.route");
+    if (c->router == MOE_ROUTER_HASH) {
+        if (launch_hash_route(token_ids, c->T, c->E, c->G, c->K, c->M, topk_idx, topk_w, s))
+            return MOE_ERR_CUDA;
+    } else if (route_affinity(*c, x, router_w, logit_offset, bias, topk_idx, topk_w, nullptr, ws, L,
+                              s)) {
+        return MOE_ERR_CUDA;
+    }
+    stage.next("moe.dispatch");
+    DispatchWs dw{at<int32_t>(ws, L.hist_t), at<int32_t>(ws, L.base_t),
+                  at<int32_t>(ws, L.send_part), at<int32_t>(ws, L.sendtok_part)};
+    // the payload and its scales share the x_perm region (d + 4 <= 2 d bytes a row);
+    // the shared experts' codes of x come out of the same pass over x
+    int8_t *x_perm_q = at<int8_t>(ws, L.x_perm);
+    float *x_scale = at<float>(ws, L.x_perm + (size_t)c->T * c->K * c->d);
+    const bool shared = c->n_shared > 0;
+    if (launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send, send_tok,
+                        perm_token, inv_perm, nullptr, dw, at<int32_t>(ws, L.status), s) ||
+        launch_gather_int8(x, inv_perm, c->T, c->d, c->K, x_perm_q, x_scale,
+                           shared ? at<int8_t>(ws, L8.x_q) : nullptr,
+                           shared ? at<float>(ws, L8.x_q_scale) : nullptr, s))
+        return MOE_ERR_CUDA;
+    stage.next("moe.expert_ffn");
+    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, ws, L8, s)) return MOE_ERR_CUDA;
+    stage.next("moe.combine");
+    return cuda_status(launch_combine(y_perm, inv_perm, topk_w, y_sh, c->T, c->d, c->K,
+                                      (int64_t)c->T * c->K, out, s));
 }
 
 }  // extern "C"

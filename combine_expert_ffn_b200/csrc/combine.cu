@@ -93,4 +93,104 @@ cudaError_t launch_combine(const void *y_perm, const int32_t *inv_perm, const fl
     return cudaGetLastError();
 }
 
+// Gradients of the combine (out_t = y_shared_t + sum_j w_j y_row(t,j)) with
+// respect to the expert rows and the gates:
+//   d_y_perm[row(t,j)] = bf16(w_(t,j) d_out[t]),  d_topk_w[t][j] = d_out[t] . y_perm[row(t,j)]
+// (y_shared's gradient is d_out itself.)  HBM-bound: per copy one row read and
+// one written, and d_out once per token: the K warps of a token run side by
+// side in a block, so that K - 1 of them find its row in L1.  WARPS warps share
+// a copy's row: one when the copies fill the GPU, eight for short batches.
+template <int WARPS, bool DY, bool DW>
+__global__ void __launch_bounds__(CB_THREADS)
+combine_backward_kernel(const uint4 *__restrict__ d_out, const uint4 *__restrict__ y_perm,
+                        const int32_t *__restrict__ inv_perm, const float *__restrict__ topk_w,
+                        int chunks, int K, int64_t copies, uint4 *__restrict__ d_y_perm,
+                        float *__restrict__ d_topk_w) {
+    constexpr int TEAM = WARPS * 32, UNROLL = 4;
+    const int64_t copy = blockIdx.x * (int64_t)(CB_THREADS / TEAM) + threadIdx.x / TEAM;
+    if (copy >= copies) return;  // whole warps; with WARPS > 1 the block is one copy
+    const int at = threadIdx.x % TEAM;
+    const int row = __ldg(inv_perm + copy);
+    const bool have = row >= 0 && row < copies;
+    float dot = 0.f;
+    if (have) {
+        const uint4 *g_row = d_out + copy / K * chunks;
+        const uint4 *y_row = y_perm + (int64_t)row * chunks;
+        uint4 *dy_row = d_y_perm + (int64_t)row * chunks;
+        const float w = DY ? __ldg(topk_w + copy) : 0.f;
+        for (int c0 = at; c0 < chunks; c0 += UNROLL * TEAM) {
+            uint4 g[UNROLL], y[UNROLL];
+#pragma unroll
+            for (int q = 0; q < UNROLL; ++q) {
+                const int c = c0 + q * TEAM;
+                g[q] = y[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < chunks) {
+                    g[q] = __ldg(g_row + c);
+                    if (DW) y[q] = __ldcs(y_row + c);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < UNROLL; ++q) {
+                const int c = c0 + q * TEAM;
+                const uint32_t gw[4] = {g[q].x, g[q].y, g[q].z, g[q].w};
+                const uint32_t yw[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float lo = bf16_lo(gw[k]), hi = bf16_hi(gw[k]);
+                    if (DY) o[k] = pack_bf16x2(w * lo, w * hi);
+                    if (DW) dot = fmaf(hi, bf16_hi(yw[k]), fmaf(lo, bf16_lo(yw[k]), dot));
+                }
+                if (DY && c < chunks) __stcs(dy_row + c, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+        }
+    }
+    if (!DW) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    if (WARPS > 1) {
+        __shared__ float part[CB_THREADS / 32];
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+        __syncthreads();
+        dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) dot += part[k];
+    }
+    if (at == 0) d_topk_w[copy] = dot;
+}
+
+namespace {
+template <int WARPS>
+void run_combine_backward(const uint4 *g, const uint4 *y, const int32_t *inv_perm,
+                          const float *topk_w, int chunks, int K, int64_t copies, uint4 *dy,
+                          float *dw, cudaStream_t st) {
+    constexpr int PER = CB_THREADS / (WARPS * 32);
+    const unsigned grid = (unsigned)((copies + PER - 1) / PER);
+    if (dy && dw)
+        combine_backward_kernel<WARPS, true, true>
+            <<<grid, CB_THREADS, 0, st>>>(g, y, inv_perm, topk_w, chunks, K, copies, dy, dw);
+    else if (dy)
+        combine_backward_kernel<WARPS, true, false>
+            <<<grid, CB_THREADS, 0, st>>>(g, y, inv_perm, topk_w, chunks, K, copies, dy, dw);
+    else
+        combine_backward_kernel<WARPS, false, true>
+            <<<grid, CB_THREADS, 0, st>>>(g, y, inv_perm, topk_w, chunks, K, copies, dy, dw);
+}
+}  // namespace
+
+cudaError_t launch_combine_backward(const void *d_out, const void *y_perm,
+                                    const int32_t *inv_perm, const float *topk_w, int T, int d,
+                                    int K, int64_t n_rows, void *d_y_perm, float *d_topk_w,
+                                    cudaStream_t st) {
+    if (T == 0 || (!d_y_perm && !d_topk_w)) return cudaSuccess;
+    const uint4 *g = static_cast<const uint4 *>(d_out), *y = static_cast<const uint4 *>(y_perm);
+    uint4 *dy = static_cast<uint4 *>(d_y_perm);
+    if (n_rows >= 148 * 16)
+        run_combine_backward<1>(g, y, inv_perm, topk_w, d / 8, K, n_rows, dy, d_topk_w, st);
+    else
+        run_combine_backward<8>(g, y, inv_perm, topk_w, d / 8, K, n_rows, dy, d_topk_w, st);
+    count_launch();
+    return cudaGetLastError();
+}
+
 }  // namespace moe

@@ -21,9 +21,12 @@ bool tensor_map_2d_bf16(CUtensorMap *m, const void *base, uint64_t rows, uint64_
 bool tensor_map_3d_bf16(CUtensorMap *m, const void *base, uint64_t n_mat, uint64_t rows,
                         uint64_t cols, uint32_t box_cols, uint32_t box_rows,
                         uint32_t swizzle_bytes = 128);
-// byte tiles (FP8 payload), row-major box without swizzle
+// byte tiles (FP8 payload: row-major box without swizzle; int8 operands: 128-byte swizzle)
 bool tensor_map_2d_u8(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
-                      uint32_t box_cols, uint32_t box_rows);
+                      uint32_t box_cols, uint32_t box_rows, uint32_t swizzle_bytes = 0);
+bool tensor_map_3d_u8(CUtensorMap *m, const void *base, uint64_t n_mat, uint64_t rows,
+                      uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+                      uint32_t swizzle_bytes);
 
 // route.cu
 cudaError_t launch_route_select(const float *scores, const float *bias, int T, int E, int G,
@@ -192,6 +195,67 @@ cudaError_t launch_hash_route(const int64_t *token_ids, int T, int E, int G, int
                               int32_t *topk_idx, float *topk_w, cudaStream_t st);
 cudaError_t launch_bias_update(const int32_t *counts, int E, int T, int K, float gamma,
                                float *bias, cudaStream_t st);
+// balance.cu: the balance loss and the router's gradient.  Tokens are cut into
+// tiles of balance_tile(T): two tiles per SM for long batches, and at least 32
+// tokens (one per lane group of a block) for short ones.  part and part_n
+// ([tiles, 2, E] each) hold the tiles' shares of the sequences that cross them.
+inline int balance_tile(int T) {
+    const int c = (int)(((int64_t)T + 2 * 148 - 1) / (2 * 148));
+    return c < 32 ? 32 : c;
+}
+cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
+                                const int32_t *offsets, int n_seq, float alpha, int T, int E,
+                                int K, int32_t *counts, float *prob, float *loss, float *part,
+                                int32_t *part_n, int32_t *status, cudaStream_t st);
+cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
+                                  const float *d_topk_w, const int32_t *offsets, int n_seq,
+                                  const int32_t *counts, const float *d_loss, float alpha, int T,
+                                  int E, int K, bool softplus, float *d_logits, int32_t *status,
+                                  cudaStream_t st);
+
+// combine.cu: gradients of the combine with respect to y_perm and the gates
+cudaError_t launch_combine_backward(const void *d_out, const void *y_perm,
+                                    const int32_t *inv_perm, const float *topk_w, int T, int d,
+                                    int K, int64_t n_rows, void *d_y_perm, float *d_topk_w,
+                                    cudaStream_t st);
+
+// quant_int8.cu: rows to int8 codes and one fp32 scale each (s = amax / 127,
+// q = rint(x / s)).  bf16 or fp32 rows of `cols` values; rows that run over n_mat
+// matrices [n_mat, rows, cols] with one scale for all of them; and the dispatch
+// gather, codes and scale of token t into the rows inv_perm[t][.] of x_perm_q (and,
+// with x_q, once in token order).
+cudaError_t launch_quantize_rows_bf16(const void *x, int64_t rows, int cols, int8_t *q,
+                                      float *scale, cudaStream_t st);
+cudaError_t launch_quantize_rows_f32(const float *x, int64_t rows, int cols, int8_t *q,
+                                     float *scale, cudaStream_t st);
+cudaError_t launch_quantize_joint_bf16(const void *x, int n_mat, int64_t rows, int cols,
+                                       int8_t *q, float *scale, cudaStream_t st);
+cudaError_t launch_gather_int8(const void *x, const int32_t *inv_perm, int T, int d, int K,
+                               int8_t *x_perm_q, float *x_scale, int8_t *x_q, float *x_q_scale,
+                               cudaStream_t st);
+
+// gemm_int8.cu: the expert FFN on int8 codes (see moe_expert_ffn_int8)
+struct FfnInt8Args {
+    int T, d, E, K, d_ff, n_shared, d_ff_shared;
+    const int8_t *x_perm_q;  // [T*K, d]
+    const float *x_scale;    // [T*K]
+    const int32_t *offsets;
+    moe_int8_weights w;
+    float *h;                // [T*K, d_ff] scratch, fp32
+    int8_t *h_q;             // [T*K, d_ff] scratch
+    float *h_scale;          // [T*K]
+    void *y_perm;            // [T*K, d] bf16
+    const int8_t *x_q;       // [T, d] the shared experts' input
+    const float *x_q_scale;  // [T]
+    float *h_shared;         // [T, n_shared * d_ff_shared] scratch
+    int8_t *h_shared_q;
+    float *h_shared_scale;
+    void *y_shared;          // [T, d] bf16
+    int32_t *status;
+    int64_t timeout_ns;
+};
+cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st);
+
 cudaError_t launch_bounded_wait_selftest(int64_t timeout_ns, int32_t *status, cudaStream_t st);
 
 }  // namespace moe

@@ -65,7 +65,7 @@ bool tensor_map_3d_bf16(CUtensorMap *m, const void *base, uint64_t n_mat, uint64
 }
 
 bool tensor_map_2d_u8(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
-                      uint32_t box_cols, uint32_t box_rows) {
+                      uint32_t box_cols, uint32_t box_rows, uint32_t swizzle_bytes) {
     if (!encode_fn()) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols};
@@ -73,7 +73,21 @@ bool tensor_map_2d_u8(CUtensorMap *m, const void *base, uint64_t rows, uint64_t 
     const cuuint32_t estr[2] = {1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       swizzle_for(swizzle_bytes), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tensor_map_3d_u8(CUtensorMap *m, const void *base, uint64_t n_mat, uint64_t rows,
+                      uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+                      uint32_t swizzle_bytes) {
+    if (!encode_fn()) return false;
+    const cuuint64_t dims[3] = {cols, rows, n_mat};
+    const cuuint64_t strides[2] = {cols, rows * cols};
+    const cuuint32_t box[3] = {box_cols, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims,
+                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle_for(swizzle_bytes), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -192,6 +192,67 @@ MOE_API moe_status moe_bias_update(const moe_config *cfg, const int32_t *counts,
                                    float *bias, void *stream);
 
 /*
+ * Balance loss of the router, per sequence, with the per-expert counts behind it
+ * (the auxiliary-loss form of balancing beside moe_bias_update; DeepSeek-V3's
+ * sequence-wise loss).  For sequence s of N_s = seq_offsets[s+1] - seq_offsets[s]
+ * tokens:
+ *   counts[s][i] = copies (t, j) of its tokens with topk_idx[t][j] = i
+ *   prob[s][i]   = 1/N_s sum_t scores[t][i] / S_t,   S_t = sum_i scores[t][i]
+ *   loss[s]      = alpha * sum_i E / (K N_s) counts[s][i] * prob[s][i]
+ * (a token whose affinities are all 0 adds nothing to prob; an empty sequence has
+ * counts, prob and loss 0).  counts of one sequence over the batch are the
+ * counts of moe_dispatch.
+ *   scores       [T, E]        fp32: the affinities, as moe_route writes them
+ *   topk_idx     [T, K]        int32
+ *   seq_offsets  [n_seq + 1]   int32, ascending in [0, T]: tokens before the first
+ *                              and behind the last belong to no sequence and are
+ *                              not read; NULL: one sequence of all T tokens
+ *                              (n_seq must be 1)
+ *   counts, prob [n_seq, E]    int32, fp32 out
+ *   loss         [n_seq]       fp32 out
+ *   ws, ws_bytes               workspace of moe_workspace_size(cfg) bytes (required);
+ *                              calls that may overlap on the GPU need one each
+ * Sums are fp32 over a fixed order (no float atomics: equal inputs give equal
+ * bits), the loss over experts fp64.  Ids outside [0, E) are not counted, and
+ * offsets outside the rule above are clamped; both are flagged
+ * MOE_ERR_DEVICE_FAULT in the status word.  n_seq == 0 is a no-op; T == 0 writes
+ * zeros.  cfg->router and cfg->payload are not consulted.
+ */
+MOE_API moe_status moe_balance_loss(const moe_config *cfg, const float *scores,
+                                    const int32_t *topk_idx, const int32_t *seq_offsets,
+                                    int32_t n_seq, float alpha, int32_t *counts, float *prob,
+                                    float *loss, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of the router: of the gates (moe_route's topk_w) and of the balance
+ * loss, with respect to the logits L = x . e_i + o_i, for cfg->router SIGMOID or
+ * SQRT_SOFTPLUS (HASH has none: MOE_ERR_INVALID_ARG).  The selection, the counts
+ * and the bias are constants.  With p = scores[t][i] / S_t, Z the sum of token t's
+ * K chosen affinities and w_j = s_j / Z its gates:
+ *   d_s[t][i]      = d_loss[s] alpha E / (K N_s^2) (counts[s][i] - sum_k counts[s][k] p_k) / S_t
+ *                    + (d_topk_w[t][j] - sum_k d_topk_w[t][k] w_k) / Z  for i = topk_idx[t][j]
+ *   d_logits[t][i] = d_s[t][i] ds/dL,  ds/dL = s (1 - s)  or  (1 - exp(-s^2)) / (2 s)
+ *   scores    [T, E]  fp32, topk_idx [T, K] int32: as moe_route wrote them
+ *   d_topk_w  [T, K]  fp32 gradient of the gates (moe_combine_backward's), or NULL:
+ *                     only the balance loss
+ *   seq_offsets, n_seq, counts, alpha: those of moe_balance_loss (counts may be any
+ *                     counts, such as sums over ranks)
+ *   d_loss    [n_seq] fp32 gradient of the losses, or NULL: only the gates
+ *                     (seq_offsets, n_seq and counts are then not read)
+ *   d_logits  [T, E]  fp32 out, every row written: a token in no sequence has only
+ *                     the gates' gradient, zero without one.  Must not overlap scores.
+ *   device_status     device int32 (or NULL) that receives MOE_ERR_DEVICE_FAULT for
+ *                     an id outside [0, E), whose gate is skipped
+ * The router weights' gradient is d_logits^T x, x's share d_logits router_w, the
+ * logit offset's the column sums.  d_topk_w and d_loss both NULL: MOE_ERR_INVALID_ARG.
+ */
+MOE_API moe_status moe_route_backward(const moe_config *cfg, const float *scores,
+                                      const int32_t *topk_idx, const float *d_topk_w,
+                                      const int32_t *seq_offsets, int32_t n_seq,
+                                      const int32_t *counts, const float *d_loss, float alpha,
+                                      float *d_logits, int32_t *device_status, void *stream);
+
+/*
  * Dispatch: stable counting sort of the T*K token copies by expert.
  *   topk_idx   [T, K]   int32 in (distinct experts per token, each < E)
  *   counts     [E]      int32 out: copies per expert
@@ -356,6 +417,24 @@ MOE_API moe_status moe_combine(const moe_config *cfg, const void *y_perm, const 
                        const float *topk_w, const void *y_shared, void *out, void *stream);
 
 /*
+ * Gradient of moe_combine: for every copy (t, j) in row r = inv_perm[t][j]
+ *   d_y_perm[r]    = bf16(topk_w[t][j] * d_out[t])
+ *   d_topk_w[t][j] = sum_c d_out[t][c] * y_perm[r][c]      (fp32)
+ * (y_shared's gradient is d_out; the dispatch's gradient, the sum of the K rows
+ * of a token, is moe_combine with gates of 1.)
+ *   d_out    [T, d] bf16, y_perm [T*K, d] bf16, inv_perm [T, K] int32 (distinct rows),
+ *   topk_w   [T, K] fp32; y_perm may be NULL without d_topk_w, topk_w without d_y_perm
+ *   d_y_perm [T*K, d] bf16 out or NULL; rows that no copy names are left as they were
+ *   d_topk_w [T, K] fp32 out or NULL; 0 for a row of inv_perm outside [0, T*K)
+ * Errors: MOE_ERR_INVALID_ARG (a required pointer NULL or not 16-byte aligned, or
+ * no output).
+ */
+MOE_API moe_status moe_combine_backward(const moe_config *cfg, const void *d_out,
+                                        const void *y_perm, const int32_t *inv_perm,
+                                        const float *topk_w, void *d_y_perm, float *d_topk_w,
+                                        void *stream);
+
+/*
  * The whole layer: route -> dispatch -> expert FFN -> combine on `stream`.
  *   out [T, d] bf16 out.  topk_idx [T,K], topk_w [T,K], counts [E],
  *   offsets [E+1], send [G,G], send_tok [G,G] are optional outputs (NULL:
@@ -417,6 +496,82 @@ MOE_API moe_status moe_forward_packed(const moe_config *cfg, const void *x, cons
                                       int32_t *topk_idx, float *topk_w, int32_t *counts,
                                       int32_t *offsets, int32_t *send, int32_t *send_tok,
                                       void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Experts in 8-bit integers: the three products of an expert on int8 codes with
+ * one fp32 scale per token row and per weight channel (the
+ * "lower-precision activations", "DeepSeek 8.7 - communication", section 4,
+ * carried into the products; the format is the library's reading).  Codes of a
+ * row:
+ *   s = amax / 127 (fp32),  q = rint(x / s) (fp32 division, nearest even)
+ * so x ~ s q; a row of zeros has s = 0 and codes 0, one that holds a NaN or an
+ * infinity s = NaN.
+ *   w_gate, w_up [E, d_ff, d] int8, w_gate_scale, w_up_scale [E, d_ff] fp32
+ *   w_down       [E, d, d_ff] int8, w_down_scale [E, d] fp32
+ *   ws_gate, ws_up [n_shared, d_ff_shared, d], ..._scale [n_shared, d_ff_shared]
+ *   ws_down      [n_shared, d, d_ff_shared], ws_down_scale [d]: one scale per
+ *                channel for all shared experts, whose outputs are one sum
+ * (the six ws_ pointers may be NULL when n_shared == 0).
+ */
+typedef struct moe_int8_weights {
+    int8_t *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
+    float *w_gate_scale, *w_up_scale, *w_down_scale;
+    float *ws_gate_scale, *ws_up_scale, *ws_down_scale;
+} moe_int8_weights;
+
+/* Workspace bytes for moe_expert_ffn_int8 and moe_forward_int8 (at least
+ * moe_workspace_size(cfg), and laid out as one, so that it serves every other
+ * entry point too); 0 if unsupported.  Monotone in T. */
+MOE_API size_t moe_int8_workspace_size(const moe_config *cfg);
+
+/* Codes and scales of bf16 weights (the layouts of moe_expert_ffn), once at load:
+ * writes the buffers of *out, which the caller allocated.  Every channel's row is
+ * quantized by the rule above (ws_down's over the n_shared matrices together). */
+MOE_API moe_status moe_quantize_weights_int8(const moe_config *cfg, const void *w_gate,
+                                             const void *w_up, const void *w_down,
+                                             const void *ws_gate, const void *ws_up,
+                                             const void *ws_down, const moe_int8_weights *out,
+                                             void *stream);
+
+/* moe_dispatch with the permuted rows as int8: x_perm_q [T*K, d] codes out,
+ * x_scale [T*K] fp32 out, other arguments as moe_dispatch.  Half the bytes of a
+ * bf16 x_perm. */
+MOE_API moe_status moe_dispatch_int8(const moe_config *cfg, const void *x,
+                                     const int32_t *topk_idx, int32_t *counts, int32_t *offsets,
+                                     int32_t *send, int32_t *send_tok, int32_t *perm_token,
+                                     int32_t *inv_perm, int8_t *x_perm_q, float *x_scale, void *ws,
+                                     size_t ws_bytes, void *stream);
+
+/*
+ * Expert FFN on int8 codes.  Per expert segment, with row scale sx and channel
+ * scales sg, su, sd:
+ *   g = sx sg (Xq Wgq^T),  u = sx su (Xq Wuq^T),  h = SiLU(g) u     in fp32
+ *   (Hq, sh) = the codes and scale of each row of h
+ *   y = bf16(sh sd (Hq Wdq^T))
+ * The products are exact 32-bit integer sums on the tensor cores.  The shared
+ * experts quantize each row of x and run as one expert of width
+ * n_shared * d_ff_shared.  Arguments as moe_expert_ffn, with the rows as x_perm_q /
+ * x_scale (moe_dispatch_int8) and the weights as *w (read on the host during the
+ * call).  ws: moe_int8_workspace_size bytes, one for each call that may overlap
+ * another on the GPU.
+ * Errors: those of moe_expert_ffn; MOE_ERR_UNSUPPORTED_SHAPE also for d, d_ff or
+ * n_shared * d_ff_shared of 131072 or more (the sums would pass 32 bits).
+ */
+MOE_API moe_status moe_expert_ffn_int8(const moe_config *cfg, const int8_t *x_perm_q,
+                                       const float *x_scale, const int32_t *offsets,
+                                       const moe_int8_weights *w, void *y_perm, const void *x,
+                                       void *y_shared, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_forward with the dispatch and the experts in int8 (moe_dispatch_int8 and
+ * moe_expert_ffn_int8, the same bits); the router reads x as it is.  cfg->payload
+ * must be bf16 (MOE_ERR_UNSUPPORTED_SHAPE otherwise).  ws: moe_int8_workspace_size
+ * bytes. */
+MOE_API moe_status moe_forward_int8(const moe_config *cfg, const void *x, const float *router_w,
+                                    const float *logit_offset, const float *bias,
+                                    const int64_t *token_ids, const moe_int8_weights *w, void *out,
+                                    int32_t *topk_idx, float *topk_w, int32_t *counts,
+                                    int32_t *offsets, int32_t *send, int32_t *send_tok, void *ws,
+                                    size_t ws_bytes, void *stream);
 
 /*
  * Expert parallelism over `world` ranks, one GPU each (the dispatch and

@@ -1,0 +1,358 @@
+"""The int8 experts on the GPU: codes and scales bit for bit, the products against 64 bits."""
+import pytest
+import torch
+
+import combine_expert_ffn_b200 as moe
+import synth
+from tests import harness as H
+from tests import int8_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def config(T, d, E, K, d_ff, n_shared=0, d_ff_shared=0, G=1, M=1, router=0):
+    return moe.MoeConfig(T, d, E, G, K, M, d_ff, n_shared, d_ff_shared, router, 0)
+
+
+def routing(T, E, K, g, skew=0.0):
+    p = torch.arange(1, E + 1, device=DEV).float() ** -skew
+    u = torch.rand(T, E, device=DEV, generator=g).clamp_min(1e-30)
+    return torch.topk(u.log() / p, K, dim=1).indices.int()
+
+
+def dispatch(cfg, x, idx, ws):
+    i32, rows = dict(dtype=torch.int32, device=DEV), cfg.T * cfg.K
+    o = {"counts": torch.empty(cfg.E, **i32), "offsets": torch.empty(cfg.E + 1, **i32),
+         "send": torch.empty(cfg.G, cfg.G, **i32), "send_tok": torch.empty(cfg.G, cfg.G, **i32),
+         "perm_token": torch.empty(rows, **i32), "inv_perm": torch.empty(cfg.T, cfg.K, **i32)}
+    q = torch.full((rows, cfg.d), 77, dtype=torch.int8, device=DEV)
+    s = torch.full((rows,), -1.0, device=DEV)
+    moe.moe_dispatch_int8(cfg, x, idx, *o.values(), q, s, ws)
+    return o, q, s
+
+
+def same(a, b):
+    """Equal bits, any NaN equal to any other."""
+    return bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+def random_weights(cfg, g):
+    """int8 codes over the whole range with -128 among them, scales of a layer of unit variance."""
+    def codes(*shape):
+        return torch.randint(-128, 128, shape, dtype=torch.int8, device=DEV, generator=g)
+
+    def scales(fan, *shape):
+        return (torch.rand(shape, device=DEV, generator=g) + 0.5) * fan ** -0.5 / 74
+
+    E, d, ff, ns, fs = cfg.E, cfg.d, cfg.d_ff, cfg.n_shared, cfg.d_ff_shared
+    w = {"w_gate": codes(E, ff, d), "w_up": codes(E, ff, d), "w_down": codes(E, d, ff),
+         "w_gate_scale": scales(d, E, ff), "w_up_scale": scales(d, E, ff),
+         "w_down_scale": scales(ff, E, d)}
+    if ns:
+        w |= {"ws_gate": codes(ns, fs, d), "ws_up": codes(ns, fs, d), "ws_down": codes(ns, d, fs),
+              "ws_gate_scale": scales(d, ns, fs), "ws_up_scale": scales(d, ns, fs),
+              "ws_down_scale": scales(ns * fs, d)}
+    return w
+
+
+# ------------------------------------------------------------------ codes
+@pytest.mark.parametrize("T,d,E,K", [(1, 64, 4, 1), (1, 7168, 16, 8), (37, 128, 8, 8),
+                                     (130, 2048, 12, 3), (64, 2112, 8, 2), (300, 576, 40, 6),
+                                     (9, 8192, 4, 2), (9, 8256, 4, 2), (5, 16448, 4, 3)])
+def test_dispatch_int8(T, d, E, K):
+    cfg, g = config(T, d, E, K, 64), gen(T + d)
+    x = (torch.randn(T, d, device=DEV, generator=g)
+         * torch.exp(2 * torch.randn(T, 1, device=DEV, generator=g))).bfloat16()
+    if T > 8:
+        x[2] = 0.0
+        x[3, 5] = float("nan")
+        x[4, 7] = float("-inf")
+        x[5] = 2.0 ** -133               # the smallest bf16
+        x[6, :] = 0.0
+        x[6, d - 1] = -3.0e38
+        x[7] = x[7, 0]                    # one value: every code +-127
+    idx = routing(T, E, K, g)
+    ws = moe.alloc_workspace(cfg)
+    o, q, s = dispatch(cfg, x, idx, ws)
+    plain = {k: torch.empty_like(v) for k, v in o.items()}
+    moe.moe_dispatch(cfg, None, idx, *plain.values(), None, ws)
+    for k in o:
+        assert torch.equal(o[k], plain[k]), k
+    rq, rs = R.quantize(x.float())
+    tok = o["perm_token"].long()
+    assert torch.equal(q.double(), rq[tok]) and same(s.double(), rs[tok, 0])
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+
+
+def test_exact_ties_round_to_the_even_code():
+    T, d = 2, 64
+    cfg = config(T, d, 4, 1, 64)
+    x = torch.arange(-32, 32, device=DEV).float() / 2  # steps of half a code: amax 16 -> no tie
+    x = torch.stack([x, torch.cat([torch.tensor([63.5], device=DEV), x[1:]])]).bfloat16()
+    _, q, s = dispatch(cfg, x, torch.zeros(T, 1, dtype=torch.int32, device=DEV),
+                       moe.alloc_workspace(cfg))
+    rq, rs = R.quantize(x.float())
+    assert torch.equal(q.double(), rq) and torch.equal(s.double(), rs[:, 0])
+    assert float(s[1]) == 0.5 and (q[1, 1:].double() == (x[1, 1:].double() / 0.5).round()).all()
+
+
+@pytest.mark.parametrize("d,d_ff,ns,fs", [(64, 64, 0, 0), (192, 2112, 1, 64), (2112, 128, 2, 64),
+                                          (320, 192, 3, 2880)])
+def test_quantize_weights(d, d_ff, ns, fs):
+    cfg, g = config(8, d, 3, 1, d_ff, ns, fs), gen(d)
+    sizes = {"w_gate": (3, d_ff, d), "w_up": (3, d_ff, d), "w_down": (3, d, d_ff)}
+    if ns:
+        sizes |= {"ws_gate": (ns, fs, d), "ws_up": (ns, fs, d), "ws_down": (ns, d, fs)}
+    w = {k: torch.randn(v, device=DEV, generator=g).bfloat16() for k, v in sizes.items()}
+    out = moe.quantize_weights_int8(cfg, *w.values()).tensors
+    for k, v in w.items():
+        if k == "ws_down":
+            q, s = R.quantize(v.permute(1, 0, 2).flatten(1).float())
+            q = q.view(d, ns, fs).permute(1, 0, 2)
+        else:
+            q, s = R.quantize(v.flatten(0, 1).float())
+            q = q.view(v.shape)
+        assert torch.equal(out[k].double(), q), k
+        assert torch.equal(out[k + "_scale"].double().flatten(), s.flatten()), k
+
+
+# ------------------------------------------------------------------ products
+FFN = [  # T, d, E, K, d_ff, n_shared, d_ff_shared, skew
+    (1, 64, 1, 1, 64, 0, 0, 0.0), (1, 7168, 16, 8, 192, 1, 64, 0.0), (2, 128, 8, 2, 128, 2, 64, 0.0),
+    (64, 192, 4, 4, 64, 3, 192, 0.0), (127, 128, 1, 1, 256, 0, 0, 0.0),
+    (128, 256, 1, 1, 320, 1, 128, 0.0), (129, 64, 2, 1, 192, 1, 320, 0.0),
+    (264, 320, 12, 4, 192, 1, 128, 0.0), (520, 192, 40, 6, 128, 2, 64, 1.2),
+    (300, 2048, 64, 6, 1408, 2, 1408, 0.6), (33, 576, 1024, 8, 64, 0, 0, 0.0),
+    (1000, 448, 6, 2, 576, 1, 576, 2.0), (16, 4096, 3, 3, 2112, 1, 4160, 0.0),
+    (700, 1024, 5, 4, 1024, 1, 512, 0.0)]
+
+
+def check_ffn(cfg, x_perm_q, x_scale, offsets, w, x, y, y_shared):
+    routed, shared = R.ffn(cfg, x_perm_q, x_scale, offsets, w, x)
+    for got, want in ((y, routed), (y_shared, shared)):
+        if want is not None:
+            off = (got.double() - want[0]).abs()
+            assert (off <= want[1]).all(), float((off / want[1]).max())
+
+
+def ffn_inputs(case, seed=0):
+    T, d, E, K, d_ff, ns, fs, skew = case
+    cfg, g = config(T, d, E, K, d_ff, ns, fs), gen(seed + sum(case[:6]))
+    idx = routing(T, E, K, g, skew)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[1:] = torch.bincount(idx.flatten().long(), minlength=E).cumsum(0)
+    xq = torch.randint(-128, 128, (T * K, d), dtype=torch.int8, device=DEV, generator=g)
+    xs = (torch.rand(T * K, device=DEV, generator=g) + 0.5) / 74
+    x = torch.randn(T, d, device=DEV, generator=g).bfloat16()
+    return cfg, xq, xs, offsets, random_weights(cfg, g), x
+
+
+def run_ffn(cfg, xq, xs, offsets, w, x, ws=None, stream=None):
+    y = torch.full(xq.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    sh = torch.full(x.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = moe.alloc_int8_workspace(cfg) if ws is None else ws
+    moe.moe_expert_ffn_int8(cfg, xq, xs, offsets, moe.Int8Weights(**w), y, x,
+                            sh if cfg.n_shared else None, ws, stream=stream)
+    return y, sh, ws
+
+
+@pytest.mark.parametrize("case", FFN, ids=str)
+def test_expert_ffn_int8(case):
+    cfg, xq, xs, offsets, w, x = ffn_inputs(case)
+    y, sh, ws = run_ffn(cfg, xq, xs, offsets, w, x)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    check_ffn(cfg, xq, xs, offsets, w, x, y, sh)
+    again, sh2, _ = run_ffn(cfg, xq, xs, offsets, w, x)
+    assert torch.equal(again, y) and (not cfg.n_shared or torch.equal(sh, sh2))
+
+
+def test_integer_sums_are_exact():
+    """Sums of small integers behind partial sums of 127 * 127 * 8191 > 2^26, which 24-bit
+    arithmetic would round away: g = u = 1, 2, 3, and the whole range of codes in w_down."""
+    T, d, d_ff = 3, 16384, 64
+    cfg = config(T, d, 1, 1, d_ff)
+    xq = torch.full((T, d), 127, dtype=torch.int8, device=DEV)
+    xq[:, -1] = torch.arange(1, T + 1, device=DEV)
+    row = torch.full((d,), 127, dtype=torch.int8, device=DEV)
+    row[8191:] = -127
+    row[-2], row[-1] = 0, 1
+    one = torch.ones(1, d_ff, device=DEV)
+    w = {"w_gate": row.expand(1, d_ff, d).contiguous(), "w_up": row.expand(1, d_ff, d).contiguous(),
+         "w_down": torch.zeros(1, d, d_ff, dtype=torch.int8, device=DEV),
+         "w_gate_scale": one, "w_up_scale": one.clone(),
+         "w_down_scale": torch.ones(1, d, device=DEV)}
+    w["w_down"][0, :, 0] = torch.arange(-128, 128, device=DEV).repeat(d // 256).to(torch.int8)
+    off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    y, _, _ = run_ffn(cfg, xq, torch.ones(T, device=DEV), off, w, x)
+    g = torch.arange(1, T + 1, device=DEV).double()[:, None]
+    want = g * torch.sigmoid(g) * g * w["w_down"][0, :, 0].double()
+    # h's row is constant: its code is 127 and its scale h / 127
+    assert ((y.double() - want).abs() <= (2.0 ** -8 + 2 * R.H_REL) * want.abs()).all()
+
+
+def test_a_row_with_a_nan_scale_is_nan_and_no_other():
+    cfg, xq, xs, offsets, w, x = ffn_inputs((70, 128, 4, 2, 192, 1, 64, 0.0))
+    y, sh, _ = run_ffn(cfg, xq, xs, offsets, w, x)
+    xs[33] = float("nan")
+    x[11, 3] = float("inf")
+    y2, sh2, _ = run_ffn(cfg, xq, xs, offsets, w, x)
+    assert y2[33].isnan().all() and sh2[11].isnan().all()
+    keep = torch.arange(140, device=DEV) != 33
+    assert torch.equal(y[keep], y2[keep])
+    keep = torch.arange(70, device=DEV) != 11
+    assert torch.equal(sh[keep], sh2[keep])
+
+
+def test_rows_of_zeros_give_zeros():
+    cfg, xq, xs, offsets, w, x = ffn_inputs((20, 64, 2, 1, 64, 1, 64, 0.0))
+    xs[4] = 0.0
+    xq[5] = 0
+    x[6] = 0.0
+    y, sh, _ = run_ffn(cfg, xq, xs, offsets, w, x)
+    assert not y[4].any() and not y[5].any() and not sh[6].any()
+
+
+def test_empty_experts_and_rows_outside_the_segments_are_left_alone():
+    cfg, xq, xs, offsets, w, x = ffn_inputs((50, 128, 8, 1, 64, 0, 0, 0.0))
+    off = torch.tensor([0, 0, 7, 7, 7, 30, 30, 41, 41], dtype=torch.int32, device=DEV)
+    y, _, ws = run_ffn(cfg, xq, xs, off, w, x)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    check_ffn(cfg, xq, xs, off, w, x, y[:41], None)
+    assert y[41:].isnan().all()  # as they were
+
+
+def test_bad_offsets_are_flagged_and_skipped():
+    cfg, xq, xs, offsets, w, x = ffn_inputs((50, 128, 4, 1, 64, 0, 0, 0.0))
+    for off in ([0, 10, 5, 20, 50], [-3, 10, 20, 30, 50], [0, 10, 20, 30, 51],
+                [0, 2 ** 31 - 1, 20, 30, 50]):
+        o = torch.tensor(off, dtype=torch.int32, device=DEV)
+        _, _, ws = run_ffn(cfg, xq, xs, o, w, x)
+        assert moe.moe_read_device_status(ws) == moe.MOE_ERR_DEVICE_FAULT, off
+
+
+# ------------------------------------------------------------------ the layer
+def layer(sh, router=0):
+    inp = synth.make_inputs(sh, DEV)
+    cfg = moe.MoeConfig.of(sh, router=router)
+    w = moe.quantize_weights_int8(cfg, *(inp[k] for k in ("w_gate", "w_up", "w_down", "ws_gate",
+                                                          "ws_up", "ws_down")))
+    return inp, cfg, w
+
+
+@pytest.mark.parametrize("name,router", [("tiny", 0), ("ragged", 0), ("ragged2", 1),
+                                         ("noshared", 0), ("ragged", 2)])
+def test_forward_int8_is_its_stages(name, router):
+    sh = H.shape(name)
+    inp, cfg, w = layer(sh, router)
+    ws = moe.alloc_int8_workspace(cfg)
+    o = moe.forward_outputs(cfg)
+    moe.moe_forward_int8(cfg, inp["x"], inp["router_w"], None, inp["bias"], w, **o, ws=ws)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    ws2 = moe.alloc_int8_workspace(cfg)
+    bf = moe.forward_outputs(cfg)
+    moe.moe_forward(cfg, inp["x"], inp["router_w"], None, inp["bias"], inp["w_gate"], inp["w_up"],
+                    inp["w_down"], inp["ws_gate"], inp["ws_up"], inp["ws_down"], **bf, ws=ws2)
+    for k in ("topk_idx", "topk_w", "counts", "offsets", "send", "send_tok"):
+        assert torch.equal(o[k], bf[k]), k
+    d, q, s = dispatch(cfg, inp["x"], o["topk_idx"], ws2)
+    y, shared, _ = run_ffn(cfg, q, s, d["offsets"], w.tensors, inp["x"], ws2)
+    out = torch.empty_like(o["out"])
+    moe.moe_combine(cfg, y, d["inv_perm"], o["topk_w"], shared if cfg.n_shared else None, out)
+    assert torch.equal(out, o["out"])
+    check_ffn(cfg, q, s, d["offsets"], w.tensors, inp["x"], y, shared)
+
+
+def test_forward_int8_is_near_the_bf16_layer():
+    """Codes are off by half a step, s / 2 = amax / 254, at most: uniform over the step, a row of
+    near-normal values (amax about 4 sigma, 6 for h) has a relative error of about
+    4 / (127 sqrt 12) = 0.9 % a factor, 1.4 % for h; of the five factors of an output (x twice, its
+    two weights, h, w_down) the squares add up to 2.5 %.  Twice that is allowed."""
+    sh = H.shape("ragged")
+    inp, cfg, w = layer(sh)
+    ws = moe.alloc_int8_workspace(cfg)
+    a, b = moe.forward_outputs(cfg), moe.forward_outputs(cfg)
+    moe.moe_forward_int8(cfg, inp["x"], inp["router_w"], None, inp["bias"], w, a["out"], ws=ws)
+    moe.moe_forward(cfg, inp["x"], inp["router_w"], None, inp["bias"], inp["w_gate"], inp["w_up"],
+                    inp["w_down"], inp["ws_gate"], inp["ws_up"], inp["ws_down"], b["out"], ws=ws)
+    frob, _ = H.compare_out(a["out"], H.bf16_to_f64(b["out"]))
+    assert frob < 0.05
+
+
+def test_forward_int8_of_one_token():
+    sh = H.shape("v3").replace(T=1, G=1, M=1, E=16, d=1024, d_ff=512, d_ff_shared=512)
+    inp, cfg, w = layer(sh)
+    ws = moe.alloc_int8_workspace(cfg)
+    o = moe.forward_outputs(cfg)
+    moe.moe_forward_int8(cfg, inp["x"], inp["router_w"], None, inp["bias"], w, **o, ws=ws)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    d, q, s = dispatch(cfg, inp["x"], o["topk_idx"], ws)
+    y, shared, _ = run_ffn(cfg, q, s, d["offsets"], w.tensors, inp["x"], ws)
+    check_ffn(cfg, q, s, d["offsets"], w.tensors, inp["x"], y, shared)
+
+
+def test_forward_int8_streams_and_graph():
+    sh = H.shape("ragged2")
+    inp, cfg, w = layer(sh)
+    ws = [moe.alloc_int8_workspace(cfg) for _ in range(2)]
+    o = [moe.forward_outputs(cfg) for _ in range(2)]
+    x2 = inp["x"].flip(0).contiguous()
+
+    def call(x, out, wsp):
+        moe.moe_forward_int8(cfg, x, inp["router_w"], None, inp["bias"], w, **out, ws=wsp)
+
+    want = []
+    for x in (inp["x"], x2):
+        call(x, o[0], ws[0])
+        want.append({k: v.clone() for k, v in o[0].items()})
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):  # two calls at once, a workspace each
+        for s, x, out, wsp in zip(streams, (inp["x"], x2), o, ws):
+            with torch.cuda.stream(s):
+                call(x, out, wsp)
+    torch.cuda.synchronize()
+    for out, ref in zip(o, want):
+        assert all(torch.equal(out[k], ref[k]) for k in ref)
+    x = inp["x"].clone()
+    graphs = []
+    for i in range(2):  # two graphs that share a workspace, replayed in turn
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(x, o[i], ws[0])
+        graphs.append(graph)
+    for _ in range(3):
+        x.copy_(inp["x"])
+        graphs[0].replay()
+        x.copy_(x2)
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    for out, ref in zip(o, want):
+        assert all(torch.equal(out[k], ref[k]) for k in ref)
+
+
+def test_python_entry_points_refuse_wrong_tensors():
+    cfg, xq, xs, offsets, w, x = ffn_inputs((8, 64, 2, 1, 64, 1, 64, 0.0))
+    ws = moe.alloc_int8_workspace(cfg)
+    y, sh = torch.empty_like(xq, dtype=torch.bfloat16), torch.empty_like(x)
+    good = moe.Int8Weights(**w)
+    for args in [(xq.float(), xs, offsets, good, y, x, sh, ws), (xq, xs.half(), offsets, good, y, x, sh, ws),
+                 (xq, xs, offsets.long(), good, y, x, sh, ws), (xq[:4], xs, offsets, good, y, x, sh, ws),
+                 (xq, xs, offsets, good, y, None, sh, ws), (xq, xs, offsets, good, y, x, None, ws),
+                 (xq.cpu(), xs, offsets, good, y, x, sh, ws), (xq, xs, offsets, good, y, x, sh, None),
+                 (xq, xs, offsets, good, y, x, sh, ws[:4096]),
+                 (xq, xs, offsets, moe.Int8Weights(**{**w, "w_up": w["w_up"][:1]}), y, x, sh, ws),
+                 (xq, xs, offsets, moe.Int8Weights(**{**w, "w_up": None}), y, x, sh, ws)]:
+        with pytest.raises(moe.MoeError):
+            moe.moe_expert_ffn_int8(cfg, *args)
+    with pytest.raises(TypeError):
+        moe.Int8Weights(w_gate=w["w_gate_scale"])
+    with pytest.raises(TypeError):
+        moe.Int8Weights(w_gate=w["w_gate"].transpose(1, 2))
+    with pytest.raises(TypeError):
+        moe.Int8Weights(gate=w["w_gate"])
