@@ -13,11 +13,26 @@
 // several times the final bf16 rounding.  The n_shared shared experts are one
 // expert of width n_shared * d_ff_shared.
 //
-// One persistent kernel per GEMM, one CTA per SM, 192 threads: warp 0 the TMA
-// producer (A 128 x 128 bytes, B 256 x 128 bytes a stage), warp 1 the MMA issuer
-// (M = 128, N = 256, K = 32), warps 2..5 the epilogue, over two accumulators so
-// that the epilogue of a tile overlaps the next tile's MMAs.  Rows of a tile past
-// its segment are computed and never stored.  Every wait is bounded.
+// Weight channels lie on the MMA's M side and token rows on N, on pairs of SMs (a
+// cluster of 2 CTAs, tcgen05.mma.cta_group::2, M = 256): a tile is one expert's
+// 256 weight rows x up to 256 tokens, in steps of 32.  CTA r holds half of the
+// weight rows (128 TMEM lanes) and loads half of the tokens, so a k block of 128
+// codes brings 32 KB into each SM for 512 cycles of MMA at N = 256, and the two
+// accumulators of 256 columns let the epilogue of a tile overlap the next one's
+// products.  An expert's tokens are cut into equal tiles of at most 256, so at
+// most 31 padding columns are computed per expert: with the tokens on M, in tiles
+// of 128, a quarter of the MMA work of a 256-token expert was padding, and a
+// decode step's (a few tokens per expert) nearly all of it.
+//   GEMM1  a tile's 256 weight rows are 128 channels' gate and up rows, 16 and 16
+//          in turn (one 16 KB TMA box over both tensors: boxes of 16 rows each made
+//          this GEMM 1.5 times slower at a decode step, 1745 against 1149 us): one
+//          half of a TMEM quarter's lanes holds a channel's gate, the other its up,
+//          and one shuffle per two tokens joins them
+//   GEMM2  256 channels; pairs of lanes exchange one of two tokens so that each
+//          stores two neighbouring channels of one
+// One persistent kernel per GEMM, 320 threads a CTA: warp 0 the TMA producer, warp
+// 1 (of the leading CTA) the MMA issuer, warps 2..9 the epilogue.  Rows of a tile
+// past its segment are computed and never stored.  Every wait is bounded.
 #include <cstring>
 
 #include "kernels.h"
@@ -25,49 +40,68 @@
 namespace moe {
 namespace gemm_i8 {
 
-constexpr int BM = 128;
-constexpr int BK = 128;      // bytes = codes per k block
-constexpr int BN_ACC = 256;  // accumulator columns
-constexpr int STAGES = 4;
-constexpr int A_BYTES = BM * BK;
-constexpr int B_BYTES = BN_ACC * BK;
+constexpr int BK = 128;            // codes (bytes) per k block
+constexpr int M_CTA = 128;         // weight rows of a CTA; the pair has twice as many
+constexpr int N_MAX = 256;         // tokens of a tile
+constexpr int N_STEP = 32;
+constexpr int STAGES = 6;
+constexpr int A_BYTES = M_CTA * BK;
+constexpr int B_BYTES = N_MAX / 2 * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int NUM_THREADS = 192;
+constexpr int EPI_WARPS = 8;       // two per TMEM lane quarter, on alternate chunks of 32 tokens
+constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_E = 1024;
 constexpr int SMEM_DYN = STAGES * STAGE_BYTES + 1024;
 
 enum { EPI_SWIGLU = 0, EPI_STORE = 1 };
+// output channels of a pair tile
 template <int EPI>
-__host__ __device__ constexpr int bn_out() { return EPI == EPI_SWIGLU ? 128 : 256; }
+__host__ __device__ constexpr int channels() { return EPI == EPI_SWIGLU ? M_CTA : 2 * M_CTA; }
 
 struct Maps {
-    CUtensorMap a_r, a_s;    // codes [rows, k], box 128 x 128
-    CUtensorMap b0_r, b1_r;  // routed weights [E, n, k], box 128 x (128 | 256): gate | down, up
-    CUtensorMap b0_s, b1_s;  // shared weights
+    CUtensorMap w_r, w_s;        // weights: gate and up as a pair, or down; 16 KB boxes
+    CUtensorMap x_r[3], x_s[3];  // token codes [rows, k], boxes of 64, 32 and 16 rows
 };
 
 struct Params {
     const int32_t *offsets;
-    int E, rows_r, T;        // T = 0: no shared experts
-    int n_out_r, n_out_s;    // output columns
-    int k_r, k_s;            // reduction lengths; the shared one is n_seg_s runs of k_s
+    int E, rows_r, T;            // T = 0: no shared experts
+    int n_out_r, n_out_s;        // output channels
+    int k_r, k_s;                // reduction lengths; the shared one is n_seg_s runs of k_s
     int n_seg_s;
-    const float *a_scale_r, *a_scale_s;    // per row
-    const float *b0_scale_r, *b1_scale_r;  // per output channel, [E, n_out_r]
-    const float *b0_scale_s, *b1_scale_s;
-    void *out_r, *out_s;     // fp32 (SwiGLU) or bf16
+    const float *x_scale_r, *x_scale_s;    // per token row
+    // per channel, [E, n_out_r]: the first and the second 16 lanes' (GEMM1), or both
+    // the same (GEMM2); gate_r, gate_s: which half holds the gate
+    const float *w0_scale_r, *w1_scale_r, *w0_scale_s, *w1_scale_s;
+    int gate_r, gate_s;
+    void *out_r, *out_s;         // fp32 (SwiGLU) or bf16
     int32_t *status;
     int64_t timeout_ns;
 };
 
 struct Tile {
-    int row0, rows_valid, n0, e, kblocks;  // e < 0: the shared experts
+    int e;           // expert, or -1: the shared experts
+    int c0;          // first channel of the pair
+    int t0, valid;   // first token row, rows to store
+    int n;           // MMA columns, a multiple of N_STEP
+    int kblocks;
 };
+
+// Token tiles of an expert: the fewest of at most N_MAX, equal up to N_STEP.
+__device__ __forceinline__ int token_tiles(int cnt) { return (cnt + N_MAX - 1) / N_MAX; }
+__device__ __forceinline__ void token_range(int cnt, int tiles, int i, Tile &t) {
+    const int units = (cnt + N_STEP - 1) / N_STEP;
+    const int each = units / tiles, more = units - each * tiles;
+    const int u0 = i * each + min(i, more);
+    t.t0 = u0 * N_STEP;
+    t.n = (each + (i < more)) * N_STEP;
+    t.valid = min(t.n, cnt - t.t0);
+}
 
 template <int EPI>
 __device__ __forceinline__ Tile decode_tile(int idx, const int *tile_base, const int *seg,
-                                            const int *segc, const Params &p, int ntr, int nt_s) {
+                                            const int *segc, const Params &p, int ntr, int nc_s) {
     Tile t;
     if (idx < ntr) {
         int lo = 0, hi = p.E;  // tile_base[lo] <= idx < tile_base[hi]
@@ -75,20 +109,19 @@ __device__ __forceinline__ Tile decode_tile(int idx, const int *tile_base, const
             const int mid = (lo + hi) >> 1;
             if (tile_base[mid] <= idx) lo = mid; else hi = mid;
         }
-        const int cnt = segc[lo], mt = (cnt + BM - 1) / BM;
+        const int cnt = segc[lo], nt = token_tiles(cnt);
         const int local = idx - tile_base[lo];
-        const int n = local / mt, m = local - n * mt;  // row tiles of a weight tile side by side
-        t.row0 = seg[lo] + m * BM;
-        t.rows_valid = min(BM, cnt - m * BM);
-        t.n0 = n * bn_out<EPI>();
+        const int c = local / nt;  // token tiles of the same weights side by side
+        token_range(cnt, nt, local - c * nt, t);
+        t.t0 += seg[lo];
+        t.c0 = c * channels<EPI>();
         t.e = lo;
         t.kblocks = (p.k_r + BK - 1) / BK;
     } else {
         const int local = idx - ntr;
-        const int m = local / nt_s, n = local - m * nt_s;
-        t.row0 = m * BM;
-        t.rows_valid = min(BM, p.T - m * BM);
-        t.n0 = n * bn_out<EPI>();
+        const int i = local / nc_s;
+        token_range(p.T, token_tiles(p.T), i, t);
+        t.c0 = (local - i * nc_s) * channels<EPI>();
         t.e = -1;
         t.kblocks = p.n_seg_s * ((p.k_s + BK - 1) / BK);
     }
@@ -108,30 +141,45 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int64_
     }
 }
 
+// A bounded wait by a converged warp: every lane sees the barrier's phase, and all
+// agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                          const Params &p) {
+    return __all_sync(0xFFFFFFFFu,
+                      mbar_wait_bounded(bar, parity, abort, p.status, p.timeout_ns));
+}
+
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return g * __frcp_rn(1.0f + __expf(-g)) * u;
+    // approximate division (2 ulp; 0 where 1 + e^-g passes 2^126): the rounded one
+    // branches, and the values of a chunk would not overlap
+    return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
 template <int EPI>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
-    constexpr int BN_OUT = bn_out<EPI>();
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
-    __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], done_bar;
+    __shared__ __align__(8) uint64_t full_bar[STAGES];   // used in the leader
+    __shared__ __align__(8) uint64_t empty_bar[STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2];
+    __shared__ __align__(8) uint64_t tempty_bar[2];      // used in the leader
+    __shared__ __align__(8) uint64_t done_bar;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     __shared__ int tile_base[MAX_E + 1], seg[MAX_E], segc[MAX_E];
+    __shared__ __align__(16) float x_scale[EPI_WARPS][N_MAX];  // a copy per warp
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const bool leader = rank == 0;
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t smem0 = smem_u32(smem);
     volatile int *abort_flag = &abort_s;
 
     if (warp == 0) {
-        // tile_base[e] = sum over experts < e of (row tiles x column tiles)
-        const int nt_r = (p.n_out_r + BN_OUT - 1) / BN_OUT;
+        // tile_base[e] = sum over experts < e of (token tiles x channel blocks)
+        const int nc_r = (p.n_out_r + channels<EPI>() - 1) / channels<EPI>();
         int carry = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
@@ -150,7 +198,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
                 seg[e] = lo;
                 segc[e] = cnt;
             }
-            const int v = (int)(((int64_t)cnt + BM - 1) / BM) * nt_r;
+            const int v = token_tiles(cnt) * nc_r;
             int incl = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -162,9 +210,8 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
         if (lane == 0) {
             tile_base[p.E] = carry;
-            tma_prefetch_desc(&maps.a_r);
-            tma_prefetch_desc(&maps.b0_r);
-            if (EPI == EPI_SWIGLU) tma_prefetch_desc(&maps.b1_r);
+            tma_prefetch_desc(&maps.w_r);
+            for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.x_r[i]);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -174,64 +221,78 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&tfull_bar[b]), 1);
-                mbar_init(smem_u32(&tempty_bar[b]), 128);
+                mbar_init(smem_u32(&tempty_bar[b]), 2 * EPI_WARPS);
             }
             mbar_init(smem_u32(&done_bar), 1);
             abort_s = 0;
             fence_barrier_init();
         }
         __syncwarp();
-        tmem_alloc<TMEM_COLS>(smem_u32(&tmem_base_s));
+        tmem_alloc_pair<TMEM_COLS>(smem_u32(&tmem_base_s));
         tc_fence_before();
     }
     __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are initialised and TMEM is allocated
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_s;
 
     const int ntr = tile_base[p.E];
-    const int mt_s = p.T > 0 ? (p.T + BM - 1) / BM : 0;
-    const int nt_s = p.T > 0 ? (p.n_out_s + BN_OUT - 1) / BN_OUT : 0;
-    const int total = ntr + mt_s * nt_s;
+    const int nc_s = p.T > 0 ? (p.n_out_s + channels<EPI>() - 1) / channels<EPI>() : 0;
+    const int total = ntr + (p.T > 0 ? token_tiles(p.T) * nc_s : 0);
+    const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
 
     if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, n_issued = 0;
-            bool ok = true;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nt_s);
-                const bool shared = t.e < 0;
-                const CUtensorMap *am = shared ? &maps.a_s : &maps.a_r;
-                const CUtensorMap *b0 = shared ? &maps.b0_s : &maps.b0_r;
-                const CUtensorMap *b1 = shared ? &maps.b1_s : &maps.b1_r;
-                const int k_len = shared ? p.k_s : p.k_r;
-                int mat = shared ? 0 : t.e, k = 0, a_col = 0;
-                for (int kb = 0; kb < t.kblocks; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag,
-                                           p.status, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&full_bar[stage]);
+        // ------------------------------------------------------ TMA producer (both CTAs)
+        // The whole warp walks the tiles and waits; one elected lane issues.
+        int stage = 0;
+        uint32_t phase = 0, n_issued = 0;
+        bool ok = true;
+        const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);  // the leader's
+        for (int idx = pair_id; idx < total && ok; idx += n_pairs) {
+            const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nc_s);
+            const bool shared = t.e < 0;
+            const CUtensorMap *w = shared ? &maps.w_s : &maps.w_r;
+            const CUtensorMap *x = shared ? maps.x_s : maps.x_r;
+            const int k_len = shared ? p.k_s : p.k_r;
+            const int ch = t.c0 + rank * (channels<EPI>() / 2);
+            const int half = t.n / 2, tok = t.t0 + rank * half;
+            // the half as boxes of 64, 32 and 16 rows
+            const int r32 = half & ~63, r16 = half & ~31;
+            const uint32_t tx = 2 * (A_BYTES + (uint32_t)half * BK);
+            int mat = shared ? 0 : t.e, k = 0, x_col = 0;
+            for (int kb = 0; kb < t.kblocks; ++kb) {
+                if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t fb = full0 + 8 * stage;
                     const uint32_t a_dst = smem0 + stage * STAGE_BYTES;
                     const uint32_t b_dst = a_dst + A_BYTES;
-                    mbar_arrive_expect_tx(fb, STAGE_BYTES);
-                    tma_load_2d(a_dst, am, fb, a_col + k, t.row0);
-                    tma_load_3d(b_dst, b0, fb, k, t.n0, mat);
-                    if (EPI == EPI_SWIGLU) tma_load_3d(b_dst + B_BYTES / 2, b1, fb, k, t.n0, mat);
-                    // a run's last block may pass its end: B reads zeros there
-                    k += BK;
-                    if (shared && k >= k_len) {
-                        k = 0;
-                        ++mat;
-                        a_col += k_len;
-                    }
-                    ++n_issued;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), tx);
+                    if (EPI == EPI_SWIGLU)
+                        tma_load_5d_pair(a_dst, w, fb, k, 0, 0, ch / 16, mat);
+                    else
+                        tma_load_3d_pair(a_dst, w, fb, k, ch, mat);
+                    if (half & 16) tma_load_2d_pair(b_dst + r16 * BK, x + 2, fb, x_col + k, tok + r16);
+                    if (half & 32) tma_load_2d_pair(b_dst + r32 * BK, x + 1, fb, x_col + k, tok + r32);
+                    if (half >= 64) tma_load_2d_pair(b_dst, x, fb, x_col + k, tok);
+                    if (half == 128) tma_load_2d_pair(b_dst + 64 * BK, x, fb, x_col + k, tok + 64);
                 }
+                __syncwarp();
+                // a run's last block may pass its end: the weights read zeros there
+                k += BK;
+                if (shared && k >= k_len) {
+                    k = 0;
+                    ++mat;
+                    x_col += k_len;
+                }
+                ++n_issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
-            // wind down: every load issued into a stage has landed
+        }
+        // wind down (leader): every load of both CTAs has landed
+        if (leader) {
             for (int s = 0; s < STAGES; ++s) {
                 if (n_issued > (uint32_t)s) {
                     const uint32_t uses = (n_issued - 1 - s) / STAGES + 1;
@@ -241,132 +302,138 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_s8_s32<BM, BN_ACC>();
+        // ------------------------------------------------------ MMA issuer (leader)
+        // The whole warp walks the tiles and waits; one elected lane issues.
+        if (leader) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nt_s);
-                if (!mbar_wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag,
-                                       p.status, p.timeout_ns))
-                    break;
+            for (int idx = pair_id; idx < total && ok; idx += n_pairs) {
+                const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nc_s);
+                const uint32_t idesc = idesc_s8_s32(2 * M_CTA, t.n);
+                if (!warp_wait(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p)) break;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * BN_ACC;
+                const uint32_t d_tmem = tmem_base + acc * N_MAX;
                 for (int kb = 0; kb < t.kblocks; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&full_bar[stage]), phase, abort_flag, p.status,
-                                           p.timeout_ns)) {
+                    if (!warp_wait(smem_u32(&full_bar[stage]), phase, abort_flag, p)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem0 + stage * STAGE_BYTES;
-                    const uint64_t a_desc = smem_desc_sw128(a_addr);
-                    const uint64_t b_desc = smem_desc_sw128(a_addr + A_BYTES);
+                    if (elect_one()) {
+                        const uint32_t a_addr = smem0 + stage * STAGE_BYTES;
+                        const uint64_t a_desc = smem_desc_sw128(a_addr);
+                        const uint64_t b_desc = smem_desc_sw128(a_addr + A_BYTES);
 #pragma unroll
-                    for (int ks = 0; ks < BK / 32; ++ks)
-                        tc_mma_s8(d_tmem, a_desc + 2 * ks, b_desc + 2 * ks, idesc,
-                                  (kb | ks) != 0 ? 1u : 0u);
-                    tc_commit(smem_u32(&empty_bar[stage]));
+                        for (int ks = 0; ks < BK / 32; ++ks)
+                            tc_mma_s8_pair(d_tmem, a_desc + 2 * ks, b_desc + 2 * ks, idesc,
+                                           (kb | ks) != 0 ? 1u : 0u);
+                        tc_commit_pair_both(smem_u32(&empty_bar[stage]));
+                    }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
-                tc_commit(smem_u32(&tfull_bar[acc]));
+                if (elect_one()) tc_commit_pair_both(smem_u32(&tfull_bar[acc]));
+                __syncwarp();
                 if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
             }
             // wind down: every MMA issued has completed
-            tc_commit(smem_u32(&done_bar));
+            if (elect_one()) tc_commit_pair(smem_u32(&done_bar));
+            __syncwarp();
             drain_wait(smem_u32(&done_bar), 0, p.timeout_ns, p.status);
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------------ epilogue
+        // ------------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;  // TMEM lane quarter this warp may access
+        const int part = (warp - 2) >> 2;
+        float *xs = x_scale[warp - 2];
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-            const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nt_s);
+        for (int idx = pair_id; idx < total; idx += n_pairs) {
+            const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nc_s);
             const bool shared = t.e < 0;
             const int n_out = shared ? p.n_out_s : p.n_out_r;
-            const int row = q * 32 + lane;
-            const bool row_ok = row < t.rows_valid;
-            const size_t grow = (size_t)t.row0 + row;
-            float sa = 0.f;
-            if (row_ok) sa = __ldg((shared ? p.a_scale_s : p.a_scale_r) + grow);
-            const size_t ch = (size_t)(shared ? 0 : t.e) * n_out + t.n0;
-            const float *s0 = (shared ? p.b0_scale_s : p.b0_scale_r) + ch;
-            const float *s1 = (shared ? p.b1_scale_s : p.b1_scale_r) + ch;
+            const float *xs_g = (shared ? p.x_scale_s : p.x_scale_r) + t.t0;
+            for (int j = lane; j < t.n; j += 32) xs[j] = j < t.valid ? __ldg(xs_g + j) : 0.f;
+            // this lane's channel (whole warps are inside or outside n_out, a multiple of 64)
+            const int ch = EPI == EPI_SWIGLU ? t.c0 + rank * 64 + q * 16 + (lane & 15)
+                                             : t.c0 + rank * 128 + q * 32 + lane;
+            const bool ch_ok = ch < n_out;
+            float ws = 0.f;
+            if (ch_ok) {
+                const float *s0 = shared ? p.w0_scale_s : p.w0_scale_r;
+                const float *s1 = shared ? p.w1_scale_s : p.w1_scale_r;
+                ws = __ldg((EPI == EPI_SWIGLU && lane >= 16 ? s1 : s0) +
+                           (size_t)(shared ? 0 : t.e) * n_out + ch);
+            }
+            __syncwarp();
             if (!mbar_wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, p.status,
                                    p.timeout_ns))
                 break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN_ACC;
-            // columns past n_out come in whole chunks: n_out is a multiple of 64
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * N_MAX;
+            // which of two neighbouring tokens this lane stores
+            const int mine = EPI == EPI_SWIGLU ? lane >> 4 : lane & 1;
+            const int partner = EPI == EPI_SWIGLU ? 16 : 1;
+            // whether this lane's own accumulator is the gate
+            const bool own_gate = mine == (shared ? p.gate_s : p.gate_r);
 #pragma unroll 1
-            for (int c = 0; c < BN_OUT && t.n0 + c < n_out; c += 32) {
-                if (EPI == EPI_SWIGLU) {
-                    uint32_t g[32], u[32];
-                    tmem_ld32(taddr + c, g);
-                    tmem_ld32(taddr + BN_ACC / 2 + c, u);
-                    tc_wait_ld();
-                    if (row_ok) {
-                        float *dst = static_cast<float *>(shared ? p.out_s : p.out_r) +
-                                     grow * n_out + t.n0 + c;
+            for (int c = part * 32; c < t.valid; c += EPI_WARPS / 4 * 32) {
+                uint32_t r[32];
+                tmem_ld32(taddr + c, r);
+                tc_wait_ld();
+                if (!ch_ok) continue;
+                // the values of a chunk first, free of branches, so that their shuffles and
+                // exponentials overlap; then its stores
+                uint32_t o[16];
 #pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            const float4 sg = __ldg(reinterpret_cast<const float4 *>(s0 + c) + v);
-                            const float4 su = __ldg(reinterpret_cast<const float4 *>(s1 + c) + v);
-                            float4 o;
-                            o.x = silu_mul((float)(int)g[4 * v] * sa * sg.x,
-                                           (float)(int)u[4 * v] * sa * su.x);
-                            o.y = silu_mul((float)(int)g[4 * v + 1] * sa * sg.y,
-                                           (float)(int)u[4 * v + 1] * sa * su.y);
-                            o.z = silu_mul((float)(int)g[4 * v + 2] * sa * sg.z,
-                                           (float)(int)u[4 * v + 2] * sa * su.z);
-                            o.w = silu_mul((float)(int)g[4 * v + 3] * sa * sg.w,
-                                           (float)(int)u[4 * v + 3] * sa * su.w);
-                            reinterpret_cast<float4 *>(dst)[v] = o;
-                        }
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 s4 = *reinterpret_cast<const float4 *>(xs + c + j);
+                    const float sx[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2) {
+                        const float a = (float)(int)r[j + h] * sx[h] * ws;
+                        const float b = (float)(int)r[j + h + 1] * sx[h + 1] * ws;
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, mine ? a : b, partner);
+                        const float own = mine ? b : a;
+                        if (EPI == EPI_SWIGLU)
+                            o[(j + h) / 2] = __float_as_uint(silu_mul(own_gate ? own : got,
+                                                                      own_gate ? got : own));
+                        else
+                            o[(j + h) / 2] = mine ? pack_bf16x2(got, own) : pack_bf16x2(own, got);
                     }
+                }
+                // fp32: one channel; bf16: two, a 4-byte word either way
+                const size_t words = EPI == EPI_SWIGLU ? (size_t)n_out : (size_t)n_out / 2;
+                uint32_t *dst = static_cast<uint32_t *>(shared ? p.out_s : p.out_r) +
+                                (size_t)(t.t0 + c + mine) * words +
+                                (EPI == EPI_SWIGLU ? ch : ch / 2);
+                if (c + 32 <= t.valid) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) dst[2 * j * words] = o[j];
                 } else {
-                    uint32_t r[32];
-                    tmem_ld32(taddr + c, r);
-                    tc_wait_ld();
-                    if (row_ok) {
-                        __nv_bfloat16 *dst =
-                            static_cast<__nv_bfloat16 *>(shared ? p.out_s : p.out_r) +
-                            grow * n_out + t.n0 + c;
-                        float f[32];
 #pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            const float4 sd = __ldg(reinterpret_cast<const float4 *>(s0 + c) + v);
-                            f[4 * v] = (float)(int)r[4 * v] * sa * sd.x;
-                            f[4 * v + 1] = (float)(int)r[4 * v + 1] * sa * sd.y;
-                            f[4 * v + 2] = (float)(int)r[4 * v + 2] * sa * sd.z;
-                            f[4 * v + 3] = (float)(int)r[4 * v + 3] * sa * sd.w;
-                        }
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            reinterpret_cast<uint4 *>(dst)[v] =
-                                make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]),
-                                           pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
-                                           pack_bf16x2(f[8 * v + 4], f[8 * v + 5]),
-                                           pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        if (c + 2 * j + mine < t.valid) dst[2 * j * words] = o[j];
                 }
             }
             tc_fence_before();
-            mbar_arrive(smem_u32(&tempty_bar[acc]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
             if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    // the leader's MMAs into this CTA's TMEM and every load into this CTA's
+    // shared memory are done before either CTA frees TMEM or exits
+    cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc<TMEM_COLS>(tmem_base);
+        tmem_dealloc_pair<TMEM_COLS>(tmem_base);
     }
 }
 
@@ -384,9 +451,39 @@ cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t st) {
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
     if (err != cudaSuccess) return err;
-    kern<<<sm_count(), NUM_THREADS, SMEM_DYN, st>>>(maps, p);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_DYN;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // one wave of pairs, one CTA per SM (pairs that do not fit at once would take
+    // their share of the tiles later)
+    cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
+    err = cudaLaunchKernelEx(&cfg, kern, maps, p);
     count_launch();
+    if (err != cudaSuccess) return err;
     return cudaGetLastError();
+}
+
+// Token codes [rows, cols] in boxes of 64, 32 and 16 rows.
+bool token_maps(CUtensorMap *x, const int8_t *q, uint64_t rows, uint64_t cols) {
+    return tensor_map_2d_u8(x, q, rows, cols, BK, 64, 128) &&
+           tensor_map_2d_u8(x + 1, q, rows, cols, BK, 32, 128) &&
+           tensor_map_2d_u8(x + 2, q, rows, cols, BK, 16, 128);
+}
+// Gate and up codes [n_mat, rows, cols] as a pair, the lower address first;
+// *gate: the place of the gate.
+bool gate_up_map(CUtensorMap *m, const int8_t *gate_w, const int8_t *up_w, uint64_t n_mat,
+                 uint64_t rows, uint64_t cols, int *gate) {
+    *gate = gate_w < up_w ? 0 : 1;
+    const int8_t *first = *gate ? up_w : gate_w, *second = *gate ? gate_w : up_w;
+    return tensor_map_pair_u8(m, first, (uint64_t)(second - first), n_mat, rows, cols, BK, 16, 4);
 }
 }  // namespace
 }  // namespace gemm_i8
@@ -401,15 +498,13 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
 
     Maps m;
     std::memset(&m, 0, sizeof(m));
-    bool ok = tensor_map_2d_u8(&m.a_r, a.x_perm_q, rows, a.d, BK, BM, 128) &&
-              tensor_map_3d_u8(&m.b0_r, a.w.w_gate, a.E, a.d_ff, a.d, BK, BN_ACC / 2, 128) &&
-              tensor_map_3d_u8(&m.b1_r, a.w.w_up, a.E, a.d_ff, a.d, BK, BN_ACC / 2, 128);
-    if (has_shared)
-        ok = ok && tensor_map_2d_u8(&m.a_s, a.x_q, a.T, a.d, BK, BM, 128) &&
-             tensor_map_3d_u8(&m.b0_s, a.w.ws_gate, 1, ffs, a.d, BK, BN_ACC / 2, 128) &&
-             tensor_map_3d_u8(&m.b1_s, a.w.ws_up, 1, ffs, a.d, BK, BN_ACC / 2, 128);
-    if (!ok) return cudaErrorInvalidValue;
     Params p{};
+    bool ok = token_maps(m.x_r, a.x_perm_q, rows, a.d) &&
+              gate_up_map(&m.w_r, a.w.w_gate, a.w.w_up, a.E, a.d_ff, a.d, &p.gate_r);
+    if (has_shared)
+        ok = ok && token_maps(m.x_s, a.x_q, a.T, a.d) &&
+             gate_up_map(&m.w_s, a.w.ws_gate, a.w.ws_up, 1, ffs, a.d, &p.gate_s);
+    if (!ok) return cudaErrorInvalidValue;
     p.offsets = a.offsets;
     p.E = a.E;
     p.rows_r = (int)rows;
@@ -418,12 +513,12 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
     p.n_out_s = ffs;
     p.k_r = p.k_s = a.d;
     p.n_seg_s = 1;
-    p.a_scale_r = a.x_scale;
-    p.a_scale_s = a.x_q_scale;
-    p.b0_scale_r = a.w.w_gate_scale;
-    p.b1_scale_r = a.w.w_up_scale;
-    p.b0_scale_s = a.w.ws_gate_scale;
-    p.b1_scale_s = a.w.ws_up_scale;
+    p.x_scale_r = a.x_scale;
+    p.x_scale_s = a.x_q_scale;
+    p.w0_scale_r = p.gate_r ? a.w.w_up_scale : a.w.w_gate_scale;
+    p.w1_scale_r = p.gate_r ? a.w.w_gate_scale : a.w.w_up_scale;
+    p.w0_scale_s = p.gate_s ? a.w.ws_up_scale : a.w.ws_gate_scale;
+    p.w1_scale_s = p.gate_s ? a.w.ws_gate_scale : a.w.ws_up_scale;
     p.out_r = a.h;
     p.out_s = a.h_shared;
     p.status = a.status;
@@ -439,20 +534,20 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
     }
 
     std::memset(&m, 0, sizeof(m));
-    ok = tensor_map_2d_u8(&m.a_r, a.h_q, rows, a.d_ff, BK, BM, 128) &&
-         tensor_map_3d_u8(&m.b0_r, a.w.w_down, a.E, a.d, a.d_ff, BK, BN_ACC, 128);
+    ok = token_maps(m.x_r, a.h_q, rows, a.d_ff) &&
+         tensor_map_3d_u8(&m.w_r, a.w.w_down, a.E, a.d, a.d_ff, BK, M_CTA, 128);
     if (has_shared)
-        ok = ok && tensor_map_2d_u8(&m.a_s, a.h_shared_q, a.T, ffs, BK, BM, 128) &&
-             tensor_map_3d_u8(&m.b0_s, a.w.ws_down, a.n_shared, a.d, a.d_ff_shared, BK, BN_ACC, 128);
+        ok = ok && token_maps(m.x_s, a.h_shared_q, a.T, ffs) &&
+             tensor_map_3d_u8(&m.w_s, a.w.ws_down, a.n_shared, a.d, a.d_ff_shared, BK, M_CTA, 128);
     if (!ok) return cudaErrorInvalidValue;
     p.n_out_r = p.n_out_s = a.d;
     p.k_r = a.d_ff;
     p.k_s = a.d_ff_shared;
     p.n_seg_s = a.n_shared;
-    p.a_scale_r = a.h_scale;
-    p.a_scale_s = a.h_shared_scale;
-    p.b0_scale_r = p.b1_scale_r = a.w.w_down_scale;
-    p.b0_scale_s = p.b1_scale_s = a.w.ws_down_scale;
+    p.x_scale_r = a.h_scale;
+    p.x_scale_s = a.h_shared_scale;
+    p.w0_scale_r = p.w1_scale_r = a.w.w_down_scale;
+    p.w0_scale_s = p.w1_scale_s = a.w.ws_down_scale;
     p.out_r = a.y_perm;
     p.out_s = a.y_shared;
     return launch<EPI_STORE>(m, p, st);

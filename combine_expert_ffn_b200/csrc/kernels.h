@@ -28,6 +28,14 @@ bool tensor_map_3d_u8(CUtensorMap *m, const void *base, uint64_t n_mat, uint64_t
                       uint64_t cols, uint32_t box_cols, uint32_t box_rows,
                       uint32_t swizzle_bytes);
 
+// two byte tensors [n_mat, rows, cols], the second `gap` bytes (below 2^40) behind the
+// first, as one of five dimensions (column, row in group, first or second, group,
+// matrix): a box brings box_groups groups of rows of both, the two in turn, with
+// 128-byte swizzle
+bool tensor_map_pair_u8(CUtensorMap *m, const void *first, uint64_t gap, uint64_t n_mat,
+                        uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t group,
+                        uint32_t box_groups);
+
 // route.cu
 cudaError_t launch_route_select(const float *scores, const float *bias, int T, int E, int G,
                                 int K, int M, int32_t *topk_idx, float *topk_w, cudaStream_t st);

@@ -91,4 +91,18 @@ bool tensor_map_3d_u8(CUtensorMap *m, const void *base, uint64_t n_mat, uint64_t
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tensor_map_pair_u8(CUtensorMap *m, const void *first, uint64_t gap, uint64_t n_mat,
+                        uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t group,
+                        uint32_t box_groups) {
+    if (!encode_fn()) return false;
+    const cuuint64_t dims[5] = {cols, group, 2, rows / group, n_mat};
+    const cuuint64_t strides[4] = {cols, gap, group * cols, rows * cols};
+    const cuuint32_t box[5] = {box_cols, group, 2, box_groups, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(first), dims,
+                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle_for(128), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
