@@ -8,8 +8,8 @@
 // shared experts' input, the SwiGLU intermediate and, once at load, the
 // weights (a row = an output channel).  HBM-bound: each row is read once and kept
 // in registers between the maximum and the rounding (rows of up to 8192 values;
-// longer ones are read twice).  A warp takes a row of up to 2048 values, a block
-// of four warps a longer one.
+// longer ones are read twice), by as many lanes as it takes to hold four 16-byte
+// loads each: a warp, four warps or a block.
 #include <type_traits>
 
 #include "kernels.h"
@@ -17,7 +17,7 @@
 namespace moe {
 namespace {
 
-constexpr int Q_THREADS = 128;
+constexpr int Q_UNITS = 4;  // 16-byte loads of a lane that stay in registers
 
 struct QuantArgs {
     const void *src;          // rows of `segs` runs of `seg_len` values
@@ -49,18 +49,55 @@ __device__ __forceinline__ uint32_t code(float x, float s) {
     return (uint32_t)(int)fminf(fmaxf(r, -127.f), 127.f) & 0xFFu;  // (a denormal s is coarse)
 }
 
-template <bool BF16, int TEAM, int UNITS>
-__global__ void __launch_bounds__(Q_THREADS)
+// The codes of N values (N / 4 words), and whether each is sure.  With inv = 1 / s,
+// x * inv is within 1.5 * 2^-23 |x / s| of the fp32 quotient, so it rounds to the same
+// code unless it lies that near a half.  Adding 1.5 * 2^23 leaves the integer, rounded
+// to nearest even, in the low byte: no conversion instructions, which run at a
+// quarter of the rate.
+// TIE: bf16 rows hold half of their largest magnitude often enough (the only
+// quotient near a half, 63.5, that 8-bit mantissas give to most rows: 1 value in 600
+// of a normal row) to be told apart: |x| = half gets at_half, 63.25 or 63.75 as the
+// division says.
+template <bool TIE, int N>
+__device__ __forceinline__ bool codes(const float (&x)[N], float inv, float half, float at_half,
+                                      uint32_t (&c)[N / 4]) {
+    constexpr float kMagic = 12582912.0f;
+    uint32_t b[N];
+    float far = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float t = TIE && fabsf(x[i]) == half ? copysignf(at_half, x[i]) : x[i] * inv;
+        const float r = t + kMagic;
+        far = fmaxf(far, fmaf(fabsf(t), 0x1p-22f, fabsf(t - (r - kMagic))));
+        b[i] = __float_as_uint(r);
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        c[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                           __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
+    return far < 0.5f;
+}
+
+template <int TEAM>
+__host__ __device__ constexpr int block_threads() { return TEAM < 128 ? 128 : TEAM; }
+
+// TEAM threads a row.
+// JOINT: rows of more than one run.
+template <bool BF16, int TEAM, bool JOINT>
+__global__ void __launch_bounds__(block_threads<TEAM>())
 quantize_rows_kernel(const QuantArgs a) {
     using U = Unit<BF16>;
+    constexpr int UNITS = Q_UNITS, Q_THREADS = block_threads<TEAM>();
     const int at = threadIdx.x % TEAM;
     const int64_t row = blockIdx.x * (int64_t)(Q_THREADS / TEAM) + threadIdx.x / TEAM;
     if (row >= a.rows) return;  // whole teams
-    const int per_seg = a.seg_len / U::N, total = per_seg * a.segs;
-    const uint4 *src = static_cast<const uint4 *>(a.src);
-    auto place = [&](int u) {  // 16-byte units from the start of src
-        const int seg = a.segs == 1 ? 0 : u / per_seg;
-        return (row * a.row_stride + seg * a.seg_stride) / U::N + (u - seg * per_seg);
+    const int per_seg = a.seg_len / U::N, total = JOINT ? per_seg * a.segs : per_seg;
+    const int64_t row0 = row * a.row_stride / U::N;  // in 16-byte units from the start of src
+    const uint4 *src = static_cast<const uint4 *>(a.src) + row0;
+    auto place = [&](int u) {
+        if (!JOINT) return (int64_t)u;
+        const int seg = u / per_seg;
+        return seg * (a.seg_stride / U::N) + (u - seg * per_seg);
     };
     uint4 v[UNITS];
     uint32_t top = 0;  // bits of the largest magnitude: NaN above infinity above the rest
@@ -93,47 +130,78 @@ quantize_rows_kernel(const QuantArgs a) {
             const int r = __ldg(a.inv_perm + row * a.K + j);
             if (r >= 0 && r < a.n_perm) a.scale_perm[r] = s;
         }
+    using Out = typename std::conditional<BF16, uint2, uint32_t>::type;
+    auto store = [&](int u, const uint32_t (&c)[U::N / 4]) {
+        Out o;
+        if constexpr (BF16) o = make_uint2(c[0], c[1]);
+        else o = c[0];
+        if (a.q) reinterpret_cast<Out *>(a.q)[row0 + place(u)] = o;
+        if (a.inv_perm)
+            for (int j = 0; j < a.K; ++j) {
+                const int r = __ldg(a.inv_perm + row * a.K + j);
+                if (r >= 0 && r < a.n_perm)
+                    reinterpret_cast<Out *>(a.q_perm)[(int64_t)r * total + u] = o;
+            }
+    };
+    // a scale whose reciprocal is no normal float (0 and NaN among them): every code
+    // is unsure, from values of inv = 0
+    const float inv = s > 0x1p-120f && s < 0x1p120f ? 1.0f / s : 0.f;
+    const float half = 0.5f * __uint_as_float(top);
+    const float at_half = rintf(__fdiv_rn(half, s)) > 63.5f ? 63.75f : 63.25f;
     const bool again = total > TEAM * UNITS;
     for (int base = 0; base < total; base += TEAM * UNITS) {
+        uint32_t unsure = 0;
 #pragma unroll
         for (int k = 0; k < UNITS; ++k) {
             const int u = base + k * TEAM + at;
             if (u >= total) continue;
             if (again) v[k] = __ldg(src + place(u));
-            uint32_t c[2] = {0u, 0u};
+            float f[U::N];
+#pragma unroll
+            for (int i = 0; i < U::N; ++i) f[i] = U::get(v[k], i);
+            uint32_t c[U::N / 4];
+            if (!codes<BF16, U::N>(f, inv, half, at_half, c) || inv == 0.f) unsure |= 1u << k;
+            else store(u, c);
+        }
+        // Units with a value near a half divide.
+        // A rolled loop that reads them again: with the divisions of every unit inlined
+        // above, the kernel's instruction fetches alone took 11 us a block.
+#pragma unroll 1
+        for (; unsure; unsure &= unsure - 1) {
+            const int u = base + (__ffs(unsure) - 1) * TEAM + at;
+            const uint4 w = __ldg(src + place(u));
+            uint32_t c[U::N / 4];
+#pragma unroll
+            for (int i = 0; i < U::N / 4; ++i) c[i] = 0u;
             if (s > 0.f) {
 #pragma unroll
-                for (int i = 0; i < U::N; ++i)
-                    c[i >> 2] |= code(U::get(v[k], i), s) << (8 * (i & 3));
+                for (int i = 0; i < U::N; ++i) c[i / 4] |= code(U::get(w, i), s) << (8 * (i % 4));
             }
-            using Out = typename std::conditional<BF16, uint2, uint32_t>::type;
-            Out o;
-            if constexpr (BF16) o = make_uint2(c[0], c[1]);
-            else o = c[0];
-            if (a.q) reinterpret_cast<Out *>(a.q)[place(u)] = o;
-            if (a.inv_perm)
-                for (int j = 0; j < a.K; ++j) {
-                    const int r = __ldg(a.inv_perm + row * a.K + j);
-                    if (r >= 0 && r < a.n_perm)
-                        reinterpret_cast<Out *>(a.q_perm)[(int64_t)r * total + u] = o;
-                }
+            store(u, c);
         }
     }
+}
+
+template <bool BF16, int TEAM>
+cudaError_t run_team(const QuantArgs &a, cudaStream_t st) {
+    constexpr int per = block_threads<TEAM>() / TEAM;
+    const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+    if (BF16 && a.segs > 1)  // the shared experts' down projection; never fp32
+        quantize_rows_kernel<BF16, TEAM, BF16><<<grid, block_threads<TEAM>(), 0, st>>>(a);
+    else
+        quantize_rows_kernel<BF16, TEAM, false><<<grid, block_threads<TEAM>(), 0, st>>>(a);
+    count_launch();
+    return cudaGetLastError();
 }
 
 template <bool BF16>
 cudaError_t run(const QuantArgs &a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
-    constexpr int UNITS = BF16 ? 8 : 16;  // 2048 values a warp, 8192 a block
-    if ((int64_t)a.segs * a.seg_len <= 2048) {
-        const int64_t per = Q_THREADS / 32;
-        quantize_rows_kernel<BF16, 32, UNITS>
-            <<<(unsigned)((a.rows + per - 1) / per), Q_THREADS, 0, st>>>(a);
-    } else {
-        quantize_rows_kernel<BF16, Q_THREADS, UNITS><<<(unsigned)a.rows, Q_THREADS, 0, st>>>(a);
-    }
-    count_launch();
-    return cudaGetLastError();
+    constexpr int WIDE = BF16 ? 256 : 512;
+    const int64_t lanes = (int64_t)a.segs * a.seg_len / (Unit<BF16>::N * Q_UNITS);
+    if (lanes <= 32) return run_team<BF16, 32>(a, st);
+    if (lanes <= 128) return run_team<BF16, 128>(a, st);
+    return run_team<BF16, WIDE>(a, st);
 }
 
 }  // namespace
