@@ -99,12 +99,10 @@ class Int8Weights(C.Structure):
     def check(self, fn, c):
         """Raises MoeError unless every tensor given has the size of configuration ``c`` and lies
         on the current GPU.  A passed configuration is remembered: the tensors never change."""
-        if not all(t is None or t.is_cuda for t in self.tensors.values()):
-            raise MoeError(fn, MOE_ERR_INVALID_ARG)
-        key = (c.d, c.E, c.d_ff, c.n_shared, c.d_ff_shared,
-               torch.cuda.current_device() if self.tensors else None)
-        if key == self.__dict__.get("_checked"):
+        key = (c.d, c.E, c.d_ff, c.n_shared, c.d_ff_shared)
+        if key == self.__dict__.get("_checked") and self._device == torch.cuda.current_device():
             return
+        k = _Call(fn, c)
         up, up_s = c.d_ff, c.n_shared * c.d_ff_shared
         sizes = {"w_gate": c.E * up * c.d, "w_up": c.E * up * c.d, "w_down": c.E * up * c.d,
                  "w_gate_scale": c.E * up, "w_up_scale": c.E * up, "w_down_scale": c.E * c.d,
@@ -112,8 +110,8 @@ class Int8Weights(C.Structure):
                  "ws_gate_scale": up_s, "ws_up_scale": up_s, "ws_down_scale": c.d}
         for n, t in self.tensors.items():
             if t is not None and (c.n_shared > 0 or not n.startswith("ws_")):
-                _tensor(fn, t, t.dtype, sizes[n])
-        self._checked = key
+                k.t(t, t.dtype, sizes[n])
+        self._checked, self._device = key, k.dev
 
 
 class MoeError(RuntimeError):
@@ -223,28 +221,50 @@ def _ws(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
-def _config(cfg):
-    return cfg if isinstance(cfg, MoeConfig) else MoeConfig.of(cfg)
+class _Call:
+    """One call of an entry point that checks its tensors: ``c`` the configuration, ``stream(s)``
+    the stream's handle, ``t(tensor, dtype, numel)`` the device pointer of a tensor that has this
+    dtype, is contiguous, holds at least ``numel`` elements and lies on the current GPU (None and
+    raw device pointers pass as they are; anything else raises MoeError).  The current device is
+    asked for once, and only where there is a tensor on a GPU."""
+    __slots__ = ("fn", "c", "dev")
+
+    def __init__(self, fn, cfg):
+        self.fn = fn
+        self.c = cfg if isinstance(cfg, MoeConfig) else MoeConfig.of(cfg)
+        self.dev = None
+
+    def t(self, t, dtype, numel):
+        if t is None or isinstance(t, int):
+            return t
+        if t.dtype is dtype and t.is_contiguous() and t.numel() >= numel and t.is_cuda:
+            if self.dev is None:
+                self.dev = torch.cuda.current_device()
+            if t.get_device() == self.dev:
+                return t.data_ptr()
+        raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
+
+    def sequences(self, seq_offsets):
+        """(device pointer, number of sequences) of a seq_offsets argument."""
+        if seq_offsets is None:
+            return None, 1
+        n = seq_offsets.numel() - 1
+        if n < 0:
+            raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
+        return self.t(seq_offsets, torch.int32, 1), n
+
+    def stream(self, stream):
+        if stream is None and self.dev is not None:
+            return _raw_stream(self.dev)
+        return _stream(stream)
 
 
-def _tensor(fn, t, dtype, numel):
-    """The device pointer of a tensor argument after checking it: dtype, contiguous, at least
-    ``numel`` elements, on the current GPU.  None and raw device pointers pass as they are."""
-    if t is None or isinstance(t, int):
-        return t
-    if (t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel or not t.is_cuda
-            or t.get_device() != torch.cuda.current_device()):
-        raise MoeError(fn, MOE_ERR_INVALID_ARG)
-    return t.data_ptr()
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _sequences(fn, seq_offsets):
-    """(device pointer, number of sequences) of a seq_offsets argument."""
-    if seq_offsets is None:
-        return None, 1
-    if seq_offsets.numel() < 1:
-        raise MoeError(fn, MOE_ERR_INVALID_ARG)
-    return _tensor(fn, seq_offsets, torch.int32, 1), seq_offsets.numel() - 1
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the handle without a Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 # ----------------------------------------------------------------- queries
@@ -350,41 +370,38 @@ def moe_permute(cfg, x, inv_perm, x_perm, stream=None) -> None:
 def moe_balance_loss(cfg, scores, topk_idx, seq_offsets, alpha, counts, prob, loss, ws,
                      stream=None) -> None:
     """Per-sequence balance loss, counts and mean affinities (seq_offsets None: one sequence)."""
-    c, fn = _config(cfg), "moe_balance_loss"
-    seq, n = _sequences(fn, seq_offsets)
+    k = _Call("moe_balance_loss", cfg)
+    c, t, f32, i32 = k.c, k.t, torch.float32, torch.int32
+    seq, n = k.sequences(seq_offsets)
     wp, wn = _ws(ws)
-    _ok(fn, _lib.moe_balance_loss(
-        C.byref(c), _tensor(fn, scores, torch.float32, c.T * c.E),
-        _tensor(fn, topk_idx, torch.int32, c.T * c.K), seq, n, alpha,
-        _tensor(fn, counts, torch.int32, n * c.E), _tensor(fn, prob, torch.float32, n * c.E),
-        _tensor(fn, loss, torch.float32, n), wp, wn, _stream(stream)))
+    _ok(k.fn, _lib.moe_balance_loss(
+        C.byref(c), t(scores, f32, c.T * c.E), t(topk_idx, i32, c.T * c.K), seq, n, alpha,
+        t(counts, i32, n * c.E), t(prob, f32, n * c.E), t(loss, f32, n), wp, wn,
+        k.stream(stream)))
 
 
 def moe_route_backward(cfg, scores, topk_idx, d_topk_w, seq_offsets, counts, d_loss, alpha,
                        d_logits, device_status=None, stream=None) -> None:
     """Gradient of the gates (d_topk_w, or None) and of the balance loss (d_loss, or None) with
     respect to the router's logits."""
-    c, fn = _config(cfg), "moe_route_backward"
-    seq, n = _sequences(fn, seq_offsets) if d_loss is not None else (None, 1)
-    _ok(fn, _lib.moe_route_backward(
-        C.byref(c), _tensor(fn, scores, torch.float32, c.T * c.E),
-        _tensor(fn, topk_idx, torch.int32, c.T * c.K),
-        _tensor(fn, d_topk_w, torch.float32, c.T * c.K), seq, n,
-        _tensor(fn, counts, torch.int32, n * c.E), _tensor(fn, d_loss, torch.float32, n), alpha,
-        _tensor(fn, d_logits, torch.float32, c.T * c.E),
-        _tensor(fn, device_status, torch.int32, 1), _stream(stream)))
+    k = _Call("moe_route_backward", cfg)
+    c, t, f32, i32 = k.c, k.t, torch.float32, torch.int32
+    seq, n = k.sequences(seq_offsets) if d_loss is not None else (None, 1)
+    _ok(k.fn, _lib.moe_route_backward(
+        C.byref(c), t(scores, f32, c.T * c.E), t(topk_idx, i32, c.T * c.K),
+        t(d_topk_w, f32, c.T * c.K), seq, n, t(counts, i32, n * c.E), t(d_loss, f32, n), alpha,
+        t(d_logits, f32, c.T * c.E), t(device_status, i32, 1), k.stream(stream)))
 
 
 def moe_combine_backward(cfg, d_out, y_perm, inv_perm, topk_w, d_y_perm, d_topk_w,
                          stream=None) -> None:
-    c, fn = _config(cfg), "moe_combine_backward"
+    k = _Call("moe_combine_backward", cfg)
+    c, t, f32, bf16 = k.c, k.t, torch.float32, torch.bfloat16
     rows = c.T * c.K
-    _ok(fn, _lib.moe_combine_backward(
-        C.byref(c), _tensor(fn, d_out, torch.bfloat16, c.T * c.d),
-        _tensor(fn, y_perm, torch.bfloat16, rows * c.d), _tensor(fn, inv_perm, torch.int32, rows),
-        _tensor(fn, topk_w, torch.float32, rows),
-        _tensor(fn, d_y_perm, torch.bfloat16, rows * c.d),
-        _tensor(fn, d_topk_w, torch.float32, rows), _stream(stream)))
+    _ok(k.fn, _lib.moe_combine_backward(
+        C.byref(c), t(d_out, bf16, c.T * c.d), t(y_perm, bf16, rows * c.d),
+        t(inv_perm, torch.int32, rows), t(topk_w, f32, rows), t(d_y_perm, bf16, rows * c.d),
+        t(d_topk_w, f32, rows), k.stream(stream)))
 
 
 # ----------------------------------------------------------------- experts in int8
@@ -405,12 +422,14 @@ def alloc_int8_workspace(cfg, device="cuda") -> torch.Tensor:
 
 def moe_quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, weights,
                               stream=None) -> None:
-    c, fn = _config(cfg), "moe_quantize_weights_int8"
-    weights.check(fn, c)
+    k = _Call("moe_quantize_weights_int8", cfg)
+    c = k.c
+    weights.check(k.fn, c)
     n, ns = c.E * c.d_ff * c.d, c.n_shared * c.d_ff_shared * c.d
-    ptrs = [_tensor(fn, t, torch.bfloat16, n) for t in (w_gate, w_up, w_down)]
-    ptrs += [_tensor(fn, t, torch.bfloat16, ns) for t in (ws_gate, ws_up, ws_down)]
-    _ok(fn, _lib.moe_quantize_weights_int8(C.byref(c), *ptrs, C.byref(weights), _stream(stream)))
+    ptrs = [k.t(w, torch.bfloat16, n) for w in (w_gate, w_up, w_down)]
+    ptrs += [k.t(w, torch.bfloat16, ns) for w in (ws_gate, ws_up, ws_down)]
+    _ok(k.fn, _lib.moe_quantize_weights_int8(C.byref(c), *ptrs, C.byref(weights),
+                                             k.stream(stream)))
 
 
 def quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None,
@@ -418,7 +437,7 @@ def quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate=None, ws_up=None, w
     """Allocates codes and scales for the bf16 weights and fills them with
     moe_quantize_weights_int8.  (On a stream that is not the current one, the caller orders the
     allocation before it.)"""
-    c = _config(cfg)
+    c = cfg if isinstance(cfg, MoeConfig) else MoeConfig.of(cfg)
     dev = w_gate.device
     ns, ffs = c.n_shared, c.d_ff_shared
     shapes = {"w_gate": (c.E, c.d_ff, c.d), "w_up": (c.E, c.d_ff, c.d), "w_down": (c.E, c.d, c.d_ff)}
@@ -435,49 +454,46 @@ def quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate=None, ws_up=None, w
 
 def moe_dispatch_int8(cfg, x, topk_idx, counts, offsets, send, send_tok, perm_token, inv_perm,
                       x_perm_q, x_scale, ws, stream=None) -> None:
-    c, fn = _config(cfg), "moe_dispatch_int8"
+    k = _Call("moe_dispatch_int8", cfg)
+    c, t, i32 = k.c, k.t, torch.int32
     wp, wn = _ws(ws)
-    rows, i32 = c.T * c.K, torch.int32
-    _ok(fn, _lib.moe_dispatch_int8(
-        C.byref(c), _tensor(fn, x, torch.bfloat16, c.T * c.d), _tensor(fn, topk_idx, i32, rows),
-        _tensor(fn, counts, i32, c.E), _tensor(fn, offsets, i32, c.E + 1),
-        _tensor(fn, send, i32, c.G * c.G), _tensor(fn, send_tok, i32, c.G * c.G),
-        _tensor(fn, perm_token, i32, rows), _tensor(fn, inv_perm, i32, rows),
-        _tensor(fn, x_perm_q, torch.int8, rows * c.d), _tensor(fn, x_scale, torch.float32, rows),
-        wp, wn, _stream(stream)))
+    rows, groups = c.T * c.K, c.G * c.G
+    _ok(k.fn, _lib.moe_dispatch_int8(
+        C.byref(c), t(x, torch.bfloat16, c.T * c.d), t(topk_idx, i32, rows), t(counts, i32, c.E),
+        t(offsets, i32, c.E + 1), t(send, i32, groups), t(send_tok, i32, groups),
+        t(perm_token, i32, rows), t(inv_perm, i32, rows), t(x_perm_q, torch.int8, rows * c.d),
+        t(x_scale, torch.float32, rows), wp, wn, k.stream(stream)))
 
 
 def moe_expert_ffn_int8(cfg, x_perm_q, x_scale, offsets, weights, y_perm, x, y_shared, ws,
                         stream=None) -> None:
     """weights: Int8Weights."""
-    c, fn = _config(cfg), "moe_expert_ffn_int8"
+    k = _Call("moe_expert_ffn_int8", cfg)
+    c, t, bf16 = k.c, k.t, torch.bfloat16
     wp, wn = _ws(ws)
     rows = c.T * c.K
-    weights.check(fn, c)
-    _ok(fn, _lib.moe_expert_ffn_int8(
-        C.byref(c), _tensor(fn, x_perm_q, torch.int8, rows * c.d),
-        _tensor(fn, x_scale, torch.float32, rows), _tensor(fn, offsets, torch.int32, c.E + 1),
-        C.byref(weights), _tensor(fn, y_perm, torch.bfloat16, rows * c.d),
-        _tensor(fn, x, torch.bfloat16, c.T * c.d),
-        _tensor(fn, y_shared, torch.bfloat16, c.T * c.d), wp, wn, _stream(stream)))
+    weights.check(k.fn, c)
+    _ok(k.fn, _lib.moe_expert_ffn_int8(
+        C.byref(c), t(x_perm_q, torch.int8, rows * c.d), t(x_scale, torch.float32, rows),
+        t(offsets, torch.int32, c.E + 1), C.byref(weights), t(y_perm, bf16, rows * c.d),
+        t(x, bf16, c.T * c.d), t(y_shared, bf16, c.T * c.d), wp, wn, k.stream(stream)))
 
 
 def moe_forward_int8(cfg, x, router_w, logit_offset, bias, weights, out, topk_idx=None,
                      topk_w=None, counts=None, offsets=None, send=None, send_tok=None, ws=None,
                      stream=None, token_ids=None) -> None:
     """weights: Int8Weights; ws: alloc_int8_workspace(cfg)."""
-    c, fn = _config(cfg), "moe_forward_int8"
+    k = _Call("moe_forward_int8", cfg)
+    c, t, i32, f32 = k.c, k.t, torch.int32, torch.float32
     wp, wn = _ws(ws)
-    rows, i32, f32 = c.T * c.K, torch.int32, torch.float32
-    weights.check(fn, c)
-    _ok(fn, _lib.moe_forward_int8(
-        C.byref(c), _tensor(fn, x, torch.bfloat16, c.T * c.d),
-        _tensor(fn, router_w, f32, c.E * c.d), _tensor(fn, logit_offset, f32, c.E),
-        _tensor(fn, bias, f32, c.E), _tensor(fn, token_ids, torch.int64, c.T), C.byref(weights),
-        _tensor(fn, out, torch.bfloat16, c.T * c.d), _tensor(fn, topk_idx, i32, rows),
-        _tensor(fn, topk_w, f32, rows), _tensor(fn, counts, i32, c.E),
-        _tensor(fn, offsets, i32, c.E + 1), _tensor(fn, send, i32, c.G * c.G),
-        _tensor(fn, send_tok, i32, c.G * c.G), wp, wn, _stream(stream)))
+    rows, groups = c.T * c.K, c.G * c.G
+    weights.check(k.fn, c)
+    _ok(k.fn, _lib.moe_forward_int8(
+        C.byref(c), t(x, torch.bfloat16, c.T * c.d), t(router_w, f32, c.E * c.d),
+        t(logit_offset, f32, c.E), t(bias, f32, c.E), t(token_ids, torch.int64, c.T),
+        C.byref(weights), t(out, torch.bfloat16, c.T * c.d), t(topk_idx, i32, rows),
+        t(topk_w, f32, rows), t(counts, i32, c.E), t(offsets, i32, c.E + 1),
+        t(send, i32, groups), t(send_tok, i32, groups), wp, wn, k.stream(stream)))
 
 
 # ----------------------------------------------------------------- expert parallelism

@@ -20,8 +20,10 @@
 // Both are one pass over the affinities and bound by HBM for long batches, by
 // launch latency for short ones.
 //
-// A token's row is held by a group of lanes (16, or 32 from 512 experts), four
-// consecutive experts per 16-byte load, so that its sums are 4 or 5 shuffles.
+// A token's row is held by a group of 8, 16 or 32 lanes (by the number of
+// experts), four consecutive experts per 16-byte load, so that a warp works on up
+// to four tokens and their sums are 3 to 5 shuffles; the next row is loaded while
+// the current one is worked on.
 // The loss keeps its running sums of p in registers: a block owns a tile of
 // consecutive tokens and closes a sequence inside it by a reduction in a fixed
 // order; a sequence that crosses tiles leaves one partial row per tile, which a
@@ -36,27 +38,30 @@ constexpr int BAL_THREADS = 512;
 constexpr int BAL_WARPS = BAL_THREADS / 32;
 constexpr int BAL_CLUSTER = 8;         // blocks that share one crossing sequence
 constexpr int BAL_JOIN_THREADS = 256;
+constexpr int GRAD_THREADS = 256;
 
 // Lanes of a token's group and values a lane loads at once.
 template <int GROUP, int VEC, int N>
 struct Row {
-    static constexpr int kGroup = GROUP, kVec = VEC, kN = N;
-    static constexpr int kGroups = BAL_THREADS / GROUP;
+    static constexpr int kGroup = GROUP, kVec = VEC, kN = N, kValues = N * VEC;
     // first of the VEC experts of this lane's q-th load
     static __device__ __forceinline__ int expert(int lane, int q) {
         return (q * GROUP + lane) * VEC;
     }
-    static __device__ __forceinline__ void load(const float *row, int lane, int E,
-                                                float (&v)[N * VEC]) {
+    // row `tok` of scores, zeros from `end` on
+    static __device__ __forceinline__ void load(const float *scores, uint32_t tok, uint32_t end,
+                                                int lane, int E, float (&v)[N * VEC]) {
+        const float *row = scores + (size_t)tok * E;
+        const bool in = tok < end;
 #pragma unroll
         for (int q = 0; q < N; ++q) {
             const int i = expert(lane, q);
             if constexpr (VEC == 4) {
                 float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < E) w = __ldg(reinterpret_cast<const float4 *>(row + i));
+                if (in && i < E) w = __ldg(reinterpret_cast<const float4 *>(row + i));
                 v[4 * q] = w.x; v[4 * q + 1] = w.y; v[4 * q + 2] = w.z; v[4 * q + 3] = w.w;
             } else {
-                v[q] = i < E ? __ldg(row + i) : 0.f;
+                v[q] = in && i < E ? __ldg(row + i) : 0.f;
             }
         }
     }
@@ -90,6 +95,22 @@ __device__ __forceinline__ int find_sequence(const int32_t *offsets, int n_seq, 
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(offsets + mid) <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+// The same by a whole warp, 32 probes at a time: the search is a chain of loads.
+__device__ __forceinline__ int warp_find_sequence(const int32_t *offsets, int n_seq, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = -1, hi = n_seq + 1;
+    while (hi - lo > 1) {
+        const int step = (int)(((int64_t)hi - lo + 32) / 33);
+        const int64_t at = lo + (int64_t)(lane + 1) * step;
+        const bool le = at < hi && __ldg(offsets + at) <= t;
+        const uint32_t no = ~__ballot_sync(0xFFFFFFFFu, le);
+        const int yes = no ? __ffs(no) - 1 : 32;  // probes up to the first that is behind t
+        const int64_t behind = lo + (int64_t)(yes + 1) * step;
+        lo += yes * step;
+        hi = behind < hi ? (int)behind : hi;
     }
     return lo;
 }
@@ -129,14 +150,15 @@ struct BalanceArgs {
 
 // One tile of tokens per block.
 template <class R>
-__global__ void __launch_bounds__(BAL_THREADS, R::kN * R::kVec <= 16 ? 2 : 1)
+__global__ void __launch_bounds__(BAL_THREADS, R::kValues <= 16 ? 2 : 1)
 balance_tile_kernel(const BalanceArgs a) {
     extern __shared__ float red[];             // [BAL_WARPS, E]
     int *hist = reinterpret_cast<int *>(red + BAL_WARPS * a.E);  // [E]
     __shared__ double scratch[BAL_WARPS];
-    constexpr int NV = R::kN * R::kVec;
+    constexpr int NV = R::kValues, GROUPS = BAL_THREADS / R::kGroup;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int glane = lane % R::kGroup, group = threadIdx.x / R::kGroup;
+    dependency_release();  // the join's blocks may take their places
     const int lo_tile = blockIdx.x * a.tile;
     const int hi_tile = (int)min((int64_t)a.T, (int64_t)lo_tile + a.tile);
 
@@ -160,7 +182,7 @@ balance_tile_kernel(const BalanceArgs a) {
     for (int t = lo_tile; t < hi_tile;) {
         int s = 0, s_lo = 0, s_hi = a.T;
         if (a.offsets) {
-            s = find_sequence(a.offsets, a.n_seq, t);
+            s = warp_find_sequence(a.offsets, a.n_seq, t);
             if (s >= a.n_seq) break;  // padding behind the last sequence
             if (s < 0) {              // ... or in front of the first
                 t = max(t + 1, __ldg(a.offsets));
@@ -177,28 +199,26 @@ balance_tile_kernel(const BalanceArgs a) {
             if (i >= 0 && i < a.E) atomicAdd(hist + i, 1);
             else record_status(a.status, MOE_ERR_DEVICE_FAULT);
         }
-        float acc[NV];
+        float acc[NV], v[NV];
 #pragma unroll
         for (int q = 0; q < NV; ++q) acc[q] = 0.f;
+        R::load(a.scores, t + group, end, glane, a.E, v);
         // whole warps stay in the loop: the sums are shuffles
-        for (uint32_t u = t; u < (uint32_t)end; u += R::kGroups) {
-            const uint32_t tok = u + group;
-            float v[NV];
-            if (tok < (uint32_t)end) {
-                R::load(a.scores + (size_t)tok * a.E, glane, a.E, v);
-            } else {
-#pragma unroll
-                for (int q = 0; q < NV; ++q) v[q] = 0.f;
-            }
+        for (uint32_t u = t; u < (uint32_t)end; u += GROUPS) {
+            float next[NV];
+            R::load(a.scores, u + GROUPS + group, end, glane, a.E, next);
             float down;
             const float inv = R::inverse_sum(v, &down);
 #pragma unroll
-            for (int q = 0; q < NV; ++q) acc[q] = fmaf(v[q], inv, acc[q]);
+            for (int q = 0; q < NV; ++q) {
+                acc[q] = fmaf(v[q], inv, acc[q]);
+                v[q] = next[q];
+            }
         }
-        if constexpr (R::kGroup == 16) {
 #pragma unroll
-            for (int q = 0; q < NV; ++q) acc[q] += __shfl_xor_sync(0xFFFFFFFFu, acc[q], 16);
-        }
+        for (int o = R::kGroup; o < 32; o <<= 1)
+#pragma unroll
+            for (int q = 0; q < NV; ++q) acc[q] += __shfl_xor_sync(0xFFFFFFFFu, acc[q], o);
         if (lane < R::kGroup) {
 #pragma unroll
             for (int q = 0; q < NV; ++q) {
@@ -236,7 +256,7 @@ balance_tile_kernel(const BalanceArgs a) {
 // The sequences that cross tiles: BAL_CLUSTER blocks for each tile but the
 // last take the sequence that starts in it and goes on, if there is one, each
 // for a share of the experts.
-__global__ void __cluster_dims__(BAL_CLUSTER, 1, 1) __launch_bounds__(BAL_JOIN_THREADS)
+__global__ void __launch_bounds__(BAL_JOIN_THREADS)
 balance_join_kernel(const BalanceArgs a) {
     constexpr int COLS = 32, PARTS = BAL_JOIN_THREADS / COLS;
     __shared__ float sp[PARTS][COLS];
@@ -247,11 +267,14 @@ balance_join_kernel(const BalanceArgs a) {
     const int lo_tile = b * a.tile, hi_tile = lo_tile + a.tile;
     int s = 0, s_lo = 0, s_hi = a.T;
     if (a.offsets) {
-        s = find_sequence(a.offsets, a.n_seq, hi_tile - 1);
-        if (s < 0 || s >= a.n_seq) return;  // the whole cluster leaves
-        sequence_range(a.offsets, s, a.T, &s_lo, &s_hi);
+        s = warp_find_sequence(a.offsets, a.n_seq, hi_tile - 1);
+        if (s < 0 || s >= a.n_seq) s_hi = 0;
+        else sequence_range(a.offsets, s, a.T, &s_lo, &s_hi);
     }
-    if (s_lo < lo_tile || s_hi <= hi_tile) return;
+    // The tiles' shares.  Blocks without a sequence wait too: what follows on the stream
+    // waits for this kernel alone.
+    dependency_wait();
+    if (s_lo < lo_tile || s_hi <= hi_tile) return;  // the whole cluster leaves
     cluster_sync_all();  // every block runs before one writes to another's shared memory
     const int last = (s_hi - 1) / a.tile;
     const int len = s_hi - s_lo;
@@ -309,43 +332,81 @@ struct RouteGradArgs {
     int32_t *status;
 };
 
-template <class R>
-__global__ void __launch_bounds__(BAL_THREADS, R::kN * R::kVec <= 16 ? 2 : 1)
+// (1 - e^-x) / (2 x), x = s^2: its Taylor series below 1/2 (the first term left out
+// is 2^-27 of it), where the difference would lose digits.
+__device__ __forceinline__ float softplus_ratio(float s) {
+    const float x = s * s;
+    float y = -1.0f / 40320.0f;
+    y = fmaf(y, x, 1.0f / 5040.0f);
+    y = fmaf(y, x, -1.0f / 720.0f);
+    y = fmaf(y, x, 1.0f / 120.0f);
+    y = fmaf(y, x, -1.0f / 24.0f);
+    y = fmaf(y, x, 1.0f / 6.0f);
+    y = fmaf(y, x, -0.5f);
+    y = fmaf(y, x, 1.0f);
+    return x < 0.5f ? 0.5f * y : __fdividef(1.0f - __expf(-x), 2.0f * x);
+}
+
+// SLOTS: gates of a lane (1 where a group has a lane for each of a token's K).
+template <class R, int SLOTS>
+__global__ void __launch_bounds__(GRAD_THREADS, R::kValues <= 16 ? 3 : 1)
 route_backward_kernel(const RouteGradArgs a) {
-    extern __shared__ float gates[];  // [groups, E]: the gates' part of a token's row
-    constexpr int NV = R::kN * R::kVec;
+    extern __shared__ float gates[];  // [GROUPS, E]: the gates' part of a token's row
+    constexpr int NV = R::kValues, GROUPS = GRAD_THREADS / R::kGroup;
     const int lane = threadIdx.x & 31, glane = lane % R::kGroup;
     const int group = threadIdx.x / R::kGroup;
     float *mine = gates + group * a.E;
     const bool gate = a.d_topk_w != nullptr, balance = a.d_loss != nullptr;
     if (gate) {
-        for (int i = threadIdx.x; i < R::kGroups * a.E; i += BAL_THREADS) gates[i] = 0.f;
+        for (int i = threadIdx.x; i < GROUPS * a.E; i += GRAD_THREADS) gates[i] = 0.f;
         __syncthreads();
     }
+    const int lo_tile = blockIdx.x * a.tile;
+    const uint32_t hi_tile = (uint32_t)min((int64_t)a.T, (int64_t)lo_tile + a.tile);
     float pull[NV];  // g_s (c_i - K N_s / E) of the current sequence
 #pragma unroll
     for (int q = 0; q < NV; ++q) pull[q] = 0.f;
     int cur_lo = 0, cur_hi = 0;  // tokens for which `pull` holds
-    const int lo_tile = blockIdx.x * a.tile;
-    const int hi_tile = (int)min((int64_t)a.T, (int64_t)lo_tile + a.tile);
     bool counted = false;        // ... and whether they lie in a sequence
-    for (uint32_t u = lo_tile; u < (uint32_t)hi_tile; u += R::kGroups) {
-        const bool in = u + group < (uint32_t)hi_tile;
-        const int tok = in ? (int)(u + group) : lo_tile;
-        float v[NV];
-        if (in) {
-            R::load(a.scores + (size_t)tok * a.E, glane, a.E, v);
-        } else {
+    float v[NV], dw[SLOTS];
+    int idx[SLOTS];
+    auto load_gates = [&](uint32_t tok, int (&i)[SLOTS], float (&d)[SLOTS]) {
 #pragma unroll
-            for (int q = 0; q < NV; ++q) v[q] = 0.f;
+        for (int h = 0; h < SLOTS; ++h) {
+            const int j = h * R::kGroup + glane;
+            const bool in = gate && tok < hi_tile && j < a.K;
+            i[h] = in ? __ldg(a.topk_idx + (size_t)tok * a.K + j) : -1;
+            d[h] = in ? __ldg(a.d_topk_w + (size_t)tok * a.K + j) : 0.f;
+            if (in && (i[h] < 0 || i[h] >= a.E)) {
+                record_status(a.status, MOE_ERR_DEVICE_FAULT);
+                i[h] = -1;
+            }
         }
-        if (balance && in && (tok < cur_lo || tok >= cur_hi)) {
-            int s = 0;
-            cur_lo = 0, cur_hi = a.T;
-            if (a.offsets) {
-                s = find_sequence(a.offsets, a.n_seq, tok);
-                cur_lo = s < 0 ? 0 : __ldg(a.offsets + s);
-                cur_hi = s >= a.n_seq ? a.T : __ldg(a.offsets + s + 1);
+    };
+    R::load(a.scores, lo_tile + group, hi_tile, glane, a.E, v);
+    load_gates(lo_tile + group, idx, dw);
+    int seq = 0;  // of the warp's first token: found by 32 probes at a time
+    if (balance && a.offsets)
+        seq = warp_find_sequence(a.offsets, a.n_seq, lo_tile + (int)(threadIdx.x & ~31u) / R::kGroup);
+    for (uint32_t u = lo_tile; u < hi_tile; u += GROUPS) {
+        const uint32_t tok = u + group;
+        const bool in = tok < hi_tile;
+        // this token's chosen affinities (its row is in L1) and the next token's loads
+        float sj[SLOTS], next[NV], next_dw[SLOTS];
+        int next_idx[SLOTS];
+#pragma unroll
+        for (int h = 0; h < SLOTS; ++h)
+            sj[h] = idx[h] >= 0 ? __ldg(a.scores + (size_t)tok * a.E + idx[h]) : 0.f;
+        R::load(a.scores, tok + GROUPS, hi_tile, glane, a.E, next);
+        load_gates(tok + GROUPS, next_idx, next_dw);
+
+        if (balance && in && ((int)tok < cur_lo || (int)tok >= cur_hi)) {
+            int s = seq;
+            for (int look = 0; look < 2; ++look) {  // the sequence at hand, else the search
+                if (look) s = find_sequence(a.offsets, a.n_seq, (int)tok);
+                cur_lo = !a.offsets || s < 0 ? 0 : __ldg(a.offsets + s);
+                cur_hi = !a.offsets || s >= a.n_seq ? a.T : __ldg(a.offsets + s + 1);
+                if (!a.offsets || ((int)tok >= cur_lo && (int)tok < cur_hi)) break;
             }
             counted = s >= 0 && s < a.n_seq;
             const int s_lo = max(0, cur_lo), len = min(a.T, cur_hi) - s_lo;
@@ -364,53 +425,74 @@ route_backward_kernel(const RouteGradArgs a) {
                                                        a.E - mean));
             }
         }
-        float down = 1.0f, inv = 0.f, dot = 0.f;
-        if (balance) {
-            inv = R::inverse_sum(v, &down);
+
+        // the four sums of a token side by side: S, pull . s, Z, dw . s_chosen
+        float sum = 0.f, dot = 0.f, z = 0.f, zdw = 0.f, down = 1.0f;
+        auto sums = [&] {
+            sum = dot = 0.f;
+            if (balance) {
 #pragma unroll
-            for (int q = 0; q < NV; ++q) dot = fmaf(pull[q], v[q], dot);
-            dot = R::sum(dot) * inv;
-        }
-        if (gate) {
-            float z = 0.f, wsum = 0.f;
-            float sj[32 / R::kGroup], dw[32 / R::kGroup];
-            int idx[32 / R::kGroup];
-#pragma unroll
-            for (int h = 0; h < 32 / R::kGroup; ++h) {
-                const int j = h * R::kGroup + glane;
-                idx[h] = -1;
-                sj[h] = dw[h] = 0.f;
-                if (in && j < a.K) {
-                    idx[h] = __ldg(a.topk_idx + (size_t)tok * a.K + j);
-                    if (idx[h] < 0 || idx[h] >= a.E) {
-                        record_status(a.status, MOE_ERR_DEVICE_FAULT);
-                        idx[h] = -1;
-                    } else {
-                        sj[h] = __ldg(a.scores + (size_t)tok * a.E + idx[h]);
-                        dw[h] = __ldg(a.d_topk_w + (size_t)tok * a.K + j);
-                    }
+                for (int q = 0; q < NV; ++q) {
+                    sum += v[q];
+                    dot = fmaf(pull[q], v[q], dot);
                 }
-                z += sj[h];
             }
-            z = R::sum(z);
-            float w[32 / R::kGroup];
+            z = zdw = 0.f;
+            if (gate) {
 #pragma unroll
-            for (int h = 0; h < 32 / R::kGroup; ++h) {
-                w[h] = z != 0.f ? __fdiv_rn(sj[h], z) : 0.f;
-                wsum = fmaf(dw[h], w[h], wsum);
+                for (int h = 0; h < SLOTS; ++h) {
+                    z += sj[h];
+                    zdw = fmaf(dw[h], sj[h], zdw);
+                }
             }
-            wsum = R::sum(wsum);
-            // added, not stored: an expert listed twice has two gates
 #pragma unroll
-            for (int h = 0; h < 32 / R::kGroup; ++h)
-                if (idx[h] >= 0) atomicAdd(mine + idx[h], (dw[h] - wsum) * w[h]);
+            for (int o = R::kGroup / 2; o > 0; o >>= 1) {
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+                z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+                zdw += __shfl_xor_sync(0xFFFFFFFFu, zdw, o);
+            }
+        };
+        sums();
+        // a row or a choice whose sum is tiny: scaled up first, or its reciprocal would
+        // overflow and its products lose digits
+        const bool tiny = (balance && fabsf(sum) < 0x1p-60f) || (gate && fabsf(z) < 0x1p-60f);
+        if (__any_sync(0xFFFFFFFFu, in && tiny)) {
+            if (balance && fabsf(sum) < 0x1p-60f) {
+                down = 0x1p-80f;
+#pragma unroll
+                for (int q = 0; q < NV; ++q) v[q] *= 0x1p80f;
+            }
+            if (gate && fabsf(z) < 0x1p-60f) {
+#pragma unroll
+                for (int h = 0; h < SLOTS; ++h) sj[h] *= 0x1p80f;
+            }
+            sums();
+        }
+        const float inv = sum != 0.f ? 1.0f / sum : 0.f, zinv = z != 0.f ? 1.0f / z : 0.f;
+        dot *= inv;
+        if (gate) {
+            // an expert listed twice has two gates: added then, stored otherwise
+            bool twice = SLOTS > 1;  // (then a lane holds several, and all are added)
+            if (SLOTS == 1) {
+                const uint32_t key = idx[0] >= 0 ? (uint32_t)(idx[0] + group * 1024)
+                                                 : 0x80000000u + lane;
+                twice = __any_sync(0xFFFFFFFFu, __popc(__match_any_sync(0xFFFFFFFFu, key)) > 1);
+            }
+#pragma unroll
+            for (int h = 0; h < SLOTS; ++h) {
+                const float g = (dw[h] - zdw * zinv) * (sj[h] * zinv);
+                if (idx[h] >= 0) {
+                    if (twice) atomicAdd(mine + idx[h], g);
+                    else mine[idx[h]] = g;
+                }
+            }
             __syncwarp();
         }
-        float o[NV];
 #pragma unroll
         for (int q = 0; q < R::kN; ++q) {
             const int i = R::expert(glane, q);
-            float gt[R::kVec];
+            float gt[R::kVec], o[R::kVec];
 #pragma unroll
             for (int k = 0; k < R::kVec; ++k) gt[k] = 0.f;
             if (gate && i < a.E) {
@@ -427,22 +509,23 @@ route_backward_kernel(const RouteGradArgs a) {
 #pragma unroll
             for (int k = 0; k < R::kVec; ++k) {
                 const int n = q * R::kVec + k;
-                const float s = v[n] * down, s2 = s * s;
+                const float s = v[n] * down;
                 float d = gt[k];
                 if (balance && counted) d = fmaf(pull[n] - dot, v[n] * inv, d);
-                const float r = a.softplus ? (s2 > 0x1p-100f ? -expm1f(-s2) / (2.0f * s2) : 0.5f)
-                                           : 1.0f - s;
-                o[n] = d != 0.f ? d * r : 0.f;  // no pull, no gradient, whatever s holds
+                const float r = a.softplus ? softplus_ratio(s) : 1.0f - s;
+                o[k] = d != 0.f ? d * r : 0.f;  // no pull, no gradient, whatever s holds
+                v[n] = next[n];
             }
             if (in && i < a.E) {
                 float *dst = a.d_logits + (size_t)tok * a.E + i;
                 if constexpr (R::kVec == 4)
-                    *reinterpret_cast<float4 *>(dst) =
-                        make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
                 else
-                    *dst = o[q];
+                    *dst = o[0];
             }
         }
+#pragma unroll
+        for (int h = 0; h < SLOTS; ++h) idx[h] = next_idx[h], dw[h] = next_dw[h];
         if (gate) __syncwarp();  // the zeroed gates are seen before the next token's
     }
 }
@@ -451,8 +534,8 @@ route_backward_kernel(const RouteGradArgs a) {
 template <class F>
 cudaError_t with_row(int E, F f) {
     if (E % 4 == 0) {
-        if (E <= 64) return f(Row<16, 4, 1>{});
-        if (E <= 128) return f(Row<16, 4, 2>{});
+        if (E <= 64) return f(Row<8, 4, 2>{});
+        if (E <= 128) return f(Row<8, 4, 4>{});
         if (E <= 256) return f(Row<16, 4, 4>{});
         if (E <= 512) return f(Row<32, 4, 4>{});
         return f(Row<32, 4, 8>{});
@@ -488,9 +571,8 @@ cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
         return cudaGetLastError();
     });
     if (err != cudaSuccess || tiles == 1) return err;
-    balance_join_kernel<<<(tiles - 1) * BAL_CLUSTER, BAL_JOIN_THREADS, 0, st>>>(a);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(balance_join_kernel, (tiles - 1) * BAL_CLUSTER, BAL_JOIN_THREADS, 0,
+                            BAL_CLUSTER, st, a);
 }
 
 cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
@@ -503,12 +585,17 @@ cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
                     T, E, K, 0, softplus, d_logits, status};
     return with_row(E, [&](auto row) {
         using R = decltype(row);
-        auto kern = route_backward_kernel<R>;
-        const size_t smem = d_topk_w ? sizeof(float) * (size_t)E * R::kGroups : 0;
+        auto kern = K <= R::kGroup ? route_backward_kernel<R, 1>
+                                   : route_backward_kernel<R, 32 / R::kGroup>;
+        constexpr int groups = GRAD_THREADS / R::kGroup;
+        const size_t smem = d_topk_w ? sizeof(float) * (size_t)E * groups : 0;
         const cudaError_t e = allow_smem(kern, smem);
         if (e != cudaSuccess) return e;
-        a.tile = balance_tile(T);
-        kern<<<(T + a.tile - 1) / a.tile, BAL_THREADS, smem, st>>>(a);
+        // consecutive tokens to a block, the same number to each of its groups: three
+        // blocks an SM for long batches, a token a group for short ones
+        const int64_t round = (int64_t)groups * 3 * 148;
+        a.tile = (int)((T + round - 1) / round) * groups;
+        kern<<<(unsigned)(((int64_t)T + a.tile - 1) / a.tile), GRAD_THREADS, smem, st>>>(a);
         count_launch();
         return cudaGetLastError();
     });

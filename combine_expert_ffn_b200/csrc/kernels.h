@@ -13,6 +13,39 @@ namespace moe {
 // Counts one kernel launch (process-wide, for moe_launch_count()).
 void count_launch();
 
+// Launches and counts kern as a dependent of the kernel before it on the stream, in
+// clusters of `cluster` blocks: it may be placed while that kernel still runs, and
+// waits for it by dependency_wait() -- in every block, since what follows on the
+// stream waits for kern alone -- before it touches what that kernel writes or reads.
+// The kernel before may let it start early by dependency_release().
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem,
+                             unsigned cluster, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, P(args)...);
+    count_launch();
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+__device__ __forceinline__ void dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dependency_release() {
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
 // tmap.cu: bf16 tensor maps, box = box_cols x box_rows (x 1), swizzle of
 // swizzle_bytes (64 or 128 = the box's row length in bytes; 0 = none)
 bool tensor_maps_available();
