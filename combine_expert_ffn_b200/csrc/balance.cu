@@ -40,6 +40,11 @@ constexpr int BAL_CLUSTER = 8;         // blocks that share one crossing sequenc
 constexpr int BAL_JOIN_THREADS = 256;
 constexpr int GRAD_THREADS = 256;
 
+// 1 / s within 1 ulp, 0 for 0 (|s| at least 2^-60: no overflow, no denormal).
+__device__ __forceinline__ float reciprocal(float s) {
+    return s != 0.f ? __fdividef(1.0f, s) : 0.f;
+}
+
 // Lanes of a token's group and values a lane loads at once.
 template <int GROUP, int VEC, int N>
 struct Row {
@@ -79,7 +84,7 @@ struct Row {
 #pragma unroll
             for (int q = 0; q < N * VEC; ++q) v[q] *= 0x1p80f;
         }
-        return s != 0.f ? 1.0f / s : 0.f;
+        return reciprocal(s);
     }
     static __device__ __forceinline__ float sum(float v) {
 #pragma unroll
@@ -327,29 +332,34 @@ struct RouteGradArgs {
     const int32_t *counts;
     const float *d_loss;     // or nullptr: no balance loss
     float alpha;
-    int T, E, K, tile, softplus;
+    int T, E, K, tile;
     float *d_logits;
     int32_t *status;
 };
 
-// (1 - e^-x) / (2 x), x = s^2: its Taylor series below 1/2 (the first term left out
-// is 2^-27 of it), where the difference would lose digits.
+// (1 - e^-x) / (2 x), x = s^2: its Taylor series below 1/4 (the first term left out
+// is 2^-24 of it), where the difference would lose digits.
 __device__ __forceinline__ float softplus_ratio(float s) {
     const float x = s * s;
-    float y = -1.0f / 40320.0f;
-    y = fmaf(y, x, 1.0f / 5040.0f);
-    y = fmaf(y, x, -1.0f / 720.0f);
-    y = fmaf(y, x, 1.0f / 120.0f);
-    y = fmaf(y, x, -1.0f / 24.0f);
-    y = fmaf(y, x, 1.0f / 6.0f);
-    y = fmaf(y, x, -0.5f);
-    y = fmaf(y, x, 1.0f);
-    return x < 0.5f ? 0.5f * y : __fdividef(1.0f - __expf(-x), 2.0f * x);
+    float y = -1.0f / 1440.0f;
+    y = fmaf(y, x, 1.0f / 240.0f);
+    y = fmaf(y, x, -1.0f / 48.0f);
+    y = fmaf(y, x, 1.0f / 12.0f);
+    y = fmaf(y, x, -0.25f);
+    y = fmaf(y, x, 0.5f);
+    return x < 0.25f ? y : __fdividef(0.5f - 0.5f * __expf(-x), x);
+}
+
+// Blocks an SM (four cost spills where a lane holds 16 values: 131072 x 256 took 62 us
+// with four, 56 with three; 196601 x 64 with 8 values 40 and 43).
+template <class R>
+__host__ __device__ constexpr int grad_blocks() {
+    return R::kValues <= 8 ? 4 : R::kValues <= 16 ? 3 : 1;
 }
 
 // SLOTS: gates of a lane (1 where a group has a lane for each of a token's K).
-template <class R, int SLOTS>
-__global__ void __launch_bounds__(GRAD_THREADS, R::kValues <= 16 ? 3 : 1)
+template <class R, int SLOTS, bool SOFTPLUS>
+__global__ void __launch_bounds__(GRAD_THREADS, grad_blocks<R>())
 route_backward_kernel(const RouteGradArgs a) {
     extern __shared__ float gates[];  // [GROUPS, E]: the gates' part of a token's row
     constexpr int NV = R::kValues, GROUPS = GRAD_THREADS / R::kGroup;
@@ -426,6 +436,12 @@ route_backward_kernel(const RouteGradArgs a) {
             }
         }
 
+        // Without a sequence `pull` and so the sums are 0: what is left to keep out of
+        // the row are values that 0 times is not 0.
+        if (!counted) {
+#pragma unroll
+            for (int q = 0; q < NV; ++q) v[q] = fabsf(v[q]) < INFINITY ? v[q] : 0.f;
+        }
         // the four sums of a token side by side: S, pull . s, Z, dw . s_chosen
         float sum = 0.f, dot = 0.f, z = 0.f, zdw = 0.f, down = 1.0f;
         auto sums = [&] {
@@ -469,7 +485,7 @@ route_backward_kernel(const RouteGradArgs a) {
             }
             sums();
         }
-        const float inv = sum != 0.f ? 1.0f / sum : 0.f, zinv = z != 0.f ? 1.0f / z : 0.f;
+        const float inv = reciprocal(sum), zinv = reciprocal(z);
         dot *= inv;
         if (gate) {
             // an expert listed twice has two gates: added then, stored otherwise
@@ -509,11 +525,8 @@ route_backward_kernel(const RouteGradArgs a) {
 #pragma unroll
             for (int k = 0; k < R::kVec; ++k) {
                 const int n = q * R::kVec + k;
-                const float s = v[n] * down;
-                float d = gt[k];
-                if (balance && counted) d = fmaf(pull[n] - dot, v[n] * inv, d);
-                const float r = a.softplus ? softplus_ratio(s) : 1.0f - s;
-                o[k] = d != 0.f ? d * r : 0.f;  // no pull, no gradient, whatever s holds
+                const float d = fmaf(pull[n] - dot, v[n] * inv, gt[k]);
+                o[k] = d * (SOFTPLUS ? softplus_ratio(v[n] * down) : fmaf(-down, v[n], 1.0f));
                 v[n] = next[n];
             }
             if (in && i < a.E) {
@@ -582,18 +595,21 @@ cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
                                   cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     RouteGradArgs a{scores, topk_idx, d_topk_w, offsets, n_seq, counts, d_loss, alpha,
-                    T, E, K, 0, softplus, d_logits, status};
+                    T, E, K, 0, d_logits, status};
     return with_row(E, [&](auto row) {
         using R = decltype(row);
-        auto kern = K <= R::kGroup ? route_backward_kernel<R, 1>
-                                   : route_backward_kernel<R, 32 / R::kGroup>;
+        constexpr int many = 32 / R::kGroup;
+        auto kern = K <= R::kGroup ? (softplus ? route_backward_kernel<R, 1, true>
+                                               : route_backward_kernel<R, 1, false>)
+                                   : (softplus ? route_backward_kernel<R, many, true>
+                                               : route_backward_kernel<R, many, false>);
         constexpr int groups = GRAD_THREADS / R::kGroup;
         const size_t smem = d_topk_w ? sizeof(float) * (size_t)E * groups : 0;
         const cudaError_t e = allow_smem(kern, smem);
         if (e != cudaSuccess) return e;
-        // consecutive tokens to a block, the same number to each of its groups: three
-        // blocks an SM for long batches, a token a group for short ones
-        const int64_t round = (int64_t)groups * 3 * 148;
+        // consecutive tokens to a block, the same number to each of its groups: one wave
+        // of blocks for long batches, a token a group for short ones
+        const int64_t round = (int64_t)groups * grad_blocks<R>() * 148;
         a.tile = (int)((T + round - 1) / round) * groups;
         kern<<<(unsigned)(((int64_t)T + a.tile - 1) / a.tile), GRAD_THREADS, smem, st>>>(a);
         count_launch();
