@@ -36,8 +36,7 @@ namespace {
 
 constexpr int BAL_THREADS = 512;
 constexpr int BAL_WARPS = BAL_THREADS / 32;
-constexpr int BAL_CLUSTER = 8;         // blocks that share one crossing sequence
-constexpr int BAL_JOIN_THREADS = 256;
+constexpr int BAL_JOIN_THREADS = 1024;
 constexpr int GRAD_THREADS = 256;
 
 // 1 / s within 1 ulp, 0 for 0 (|s| at least 2^-60: no overflow, no denormal).
@@ -63,10 +62,10 @@ struct Row {
             const int i = expert(lane, q);
             if constexpr (VEC == 4) {
                 float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (in && i < E) w = __ldg(reinterpret_cast<const float4 *>(row + i));
+                if (in && i < E) w = *reinterpret_cast<const float4 *>(row + i);
                 v[4 * q] = w.x; v[4 * q + 1] = w.y; v[4 * q + 2] = w.z; v[4 * q + 3] = w.w;
             } else {
-                v[q] = in && i < E ? __ldg(row + i) : 0.f;
+                v[q] = in && i < E ? row[i] : 0.f;
             }
         }
     }
@@ -99,7 +98,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *offsets, int n_seq, 
     int lo = -1, hi = n_seq + 1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(offsets + mid) <= t) lo = mid; else hi = mid;
+        if (offsets[mid] <= t) lo = mid; else hi = mid;
     }
     return lo;
 }
@@ -110,7 +109,7 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t *offsets, int n_
     while (hi - lo > 1) {
         const int step = (int)(((int64_t)hi - lo + 32) / 33);
         const int64_t at = lo + (int64_t)(lane + 1) * step;
-        const bool le = at < hi && __ldg(offsets + at) <= t;
+        const bool le = at < hi && offsets[at] <= t;
         const uint32_t no = ~__ballot_sync(0xFFFFFFFFu, le);
         const int yes = no ? __ffs(no) - 1 : 32;  // probes up to the first that is behind t
         const int64_t behind = lo + (int64_t)(yes + 1) * step;
@@ -124,8 +123,8 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t *offsets, int n_
 // sequence of all T tokens.
 __device__ __forceinline__ void sequence_range(const int32_t *offsets, int s, int T, int *lo,
                                                int *hi) {
-    *lo = offsets ? max(0, min(T, __ldg(offsets + s))) : 0;
-    *hi = offsets ? max(0, min(T, __ldg(offsets + s + 1))) : T;
+    *lo = offsets ? max(0, min(T, offsets[s])) : 0;
+    *hi = offsets ? max(0, min(T, offsets[s + 1])) : T;
 }
 
 // Sum over the block in a fixed order; every thread gets it.
@@ -163,6 +162,7 @@ balance_tile_kernel(const BalanceArgs a) {
     constexpr int NV = R::kValues, GROUPS = BAL_THREADS / R::kGroup;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int glane = lane % R::kGroup, group = threadIdx.x / R::kGroup;
+    dependency_wait();
     dependency_release();  // the join's blocks may take their places
     const int lo_tile = blockIdx.x * a.tile;
     const int hi_tile = (int)min((int64_t)a.T, (int64_t)lo_tile + a.tile);
@@ -171,7 +171,7 @@ balance_tile_kernel(const BalanceArgs a) {
     for (int s = blockIdx.x * BAL_WARPS + warp; s < a.n_seq; s += gridDim.x * BAL_WARPS) {
         int lo = 0, hi = a.T;
         if (a.offsets) {
-            lo = __ldg(a.offsets + s), hi = __ldg(a.offsets + s + 1);
+            lo = a.offsets[s], hi = a.offsets[s + 1];
             if (lane == 0 && (lo < 0 || hi < lo || hi > a.T))
                 record_status(a.status, MOE_ERR_DEVICE_FAULT);
             sequence_range(a.offsets, s, a.T, &lo, &hi);
@@ -190,7 +190,7 @@ balance_tile_kernel(const BalanceArgs a) {
             s = warp_find_sequence(a.offsets, a.n_seq, t);
             if (s >= a.n_seq) break;  // padding behind the last sequence
             if (s < 0) {              // ... or in front of the first
-                t = max(t + 1, __ldg(a.offsets));
+                t = max(t + 1, a.offsets[0]);
                 continue;
             }
             sequence_range(a.offsets, s, a.T, &s_lo, &s_hi);
@@ -200,7 +200,7 @@ balance_tile_kernel(const BalanceArgs a) {
         __syncthreads();
         for (int64_t c = (int64_t)t * a.K + threadIdx.x; c < (int64_t)end * a.K;
              c += BAL_THREADS) {
-            const int i = __ldg(a.topk_idx + c);
+            const int i = a.topk_idx[c];
             if (i >= 0 && i < a.E) atomicAdd(hist + i, 1);
             else record_status(a.status, MOE_ERR_DEVICE_FAULT);
         }
@@ -258,17 +258,15 @@ balance_tile_kernel(const BalanceArgs a) {
     }
 }
 
-// The sequences that cross tiles: BAL_CLUSTER blocks for each tile but the
-// last take the sequence that starts in it and goes on, if there is one, each
-// for a share of the experts.
+// The sequences that cross tiles: a block for each tile but the last takes the
+// sequence that starts in it and goes on, if there is one.  Threads lie over the
+// experts and, where these are fewer, over equal shares of the tiles.
 __global__ void __launch_bounds__(BAL_JOIN_THREADS)
 balance_join_kernel(const BalanceArgs a) {
-    constexpr int COLS = 32, PARTS = BAL_JOIN_THREADS / COLS;
-    __shared__ float sp[PARTS][COLS];
-    __shared__ int sn[PARTS][COLS];
+    __shared__ float sp[BAL_JOIN_THREADS];
+    __shared__ int sn[BAL_JOIN_THREADS];
     __shared__ double scratch[BAL_JOIN_THREADS / 32];
-    __shared__ double shared_dot[BAL_CLUSTER];
-    const int b = blockIdx.x / BAL_CLUSTER, rank = blockIdx.x % BAL_CLUSTER;
+    const int b = blockIdx.x;
     const int lo_tile = b * a.tile, hi_tile = lo_tile + a.tile;
     int s = 0, s_lo = 0, s_hi = a.T;
     if (a.offsets) {
@@ -279,48 +277,35 @@ balance_join_kernel(const BalanceArgs a) {
     // The tiles' shares.  Blocks without a sequence wait too: what follows on the stream
     // waits for this kernel alone.
     dependency_wait();
-    if (s_lo < lo_tile || s_hi <= hi_tile) return;  // the whole cluster leaves
-    cluster_sync_all();  // every block runs before one writes to another's shared memory
+    if (s_lo < lo_tile || s_hi <= hi_tile) return;
     const int last = (s_hi - 1) / a.tile;
     const int len = s_hi - s_lo;
-    const int col = threadIdx.x % COLS, part = threadIdx.x / COLS;
-    double dot = 0.0;
-    for (int i0 = rank * COLS; i0 < a.E; i0 += BAL_CLUSTER * COLS) {
-        const int i = i0 + col;
-        float p = 0.f;
-        int n = 0;
-        if (i < a.E) {
+    const int cols = (a.E + 31) / 32 * 32;  // at most 1024
+    const int parts = BAL_JOIN_THREADS / cols;
+    const int part = threadIdx.x / cols, i = threadIdx.x - part * cols;
+    float p = 0.f;
+    int n = 0;
+    if (i < a.E && part < parts) {
 #pragma unroll 8
-            for (int k = b + part; k <= last; k += PARTS) {
-                const size_t at = ((size_t)k * 2 + (k == b)) * a.E + i;
-                p += a.part[at];
-                n += a.part_n[at];
-            }
+        for (int k = b + part; k <= last; k += parts) {
+            const size_t at = ((size_t)k * 2 + (k == b)) * a.E + i;
+            p += a.part[at];
+            n += a.part_n[at];
         }
-        sp[part][col] = p;
-        sn[part][col] = n;
-        __syncthreads();
-        if (part == 0 && i < a.E) {
-            p = 0.f, n = 0;
-#pragma unroll
-            for (int k = 0; k < PARTS; ++k) p += sp[k][col], n += sn[k][col];
-            a.counts[(size_t)s * a.E + i] = n;
-            a.prob[(size_t)s * a.E + i] = p / (float)len;
-            dot += (double)n * p;
-        }
-        __syncthreads();
+    }
+    sp[threadIdx.x] = p;
+    sn[threadIdx.x] = n;
+    __syncthreads();
+    double dot = 0.0;
+    if (part == 0 && i < a.E) {
+        for (int k = 1; k < parts; ++k) p += sp[k * cols + i], n += sn[k * cols + i];
+        a.counts[(size_t)s * a.E + i] = n;
+        a.prob[(size_t)s * a.E + i] = p / (float)len;
+        dot = (double)n * p;
     }
     dot = block_sum(dot, scratch);
-    if (threadIdx.x == 0) {  // rank 0 adds the shares in rank order
-        const uint32_t to = mapa_shared(smem_u32(&shared_dot[rank]), 0);
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(dot) : "memory");
-    }
-    cluster_sync_all();
-    if (rank == 0 && threadIdx.x == 0) {
-        double total = 0.0;
-        for (int r = 0; r < BAL_CLUSTER; ++r) total += shared_dot[r];
-        a.loss[s] = (float)((double)a.alpha * a.E / ((double)a.K * len * len) * total);
-    }
+    if (threadIdx.x == 0)
+        a.loss[s] = (float)((double)a.alpha * a.E / ((double)a.K * len * len) * dot);
 }
 
 struct RouteGradArgs {
@@ -385,14 +370,16 @@ route_backward_kernel(const RouteGradArgs a) {
         for (int h = 0; h < SLOTS; ++h) {
             const int j = h * R::kGroup + glane;
             const bool in = gate && tok < hi_tile && j < a.K;
-            i[h] = in ? __ldg(a.topk_idx + (size_t)tok * a.K + j) : -1;
-            d[h] = in ? __ldg(a.d_topk_w + (size_t)tok * a.K + j) : 0.f;
+            i[h] = in ? a.topk_idx[(size_t)tok * a.K + j] : -1;
+            d[h] = in ? a.d_topk_w[(size_t)tok * a.K + j] : 0.f;
             if (in && (i[h] < 0 || i[h] >= a.E)) {
                 record_status(a.status, MOE_ERR_DEVICE_FAULT);
                 i[h] = -1;
             }
         }
     };
+    dependency_wait();
+    dependency_release();
     R::load(a.scores, lo_tile + group, hi_tile, glane, a.E, v);
     load_gates(lo_tile + group, idx, dw);
     int seq = 0;  // of the warp's first token: found by 32 probes at a time
@@ -406,7 +393,7 @@ route_backward_kernel(const RouteGradArgs a) {
         int next_idx[SLOTS];
 #pragma unroll
         for (int h = 0; h < SLOTS; ++h)
-            sj[h] = idx[h] >= 0 ? __ldg(a.scores + (size_t)tok * a.E + idx[h]) : 0.f;
+            sj[h] = idx[h] >= 0 ? a.scores[(size_t)tok * a.E + idx[h]] : 0.f;
         R::load(a.scores, tok + GROUPS, hi_tile, glane, a.E, next);
         load_gates(tok + GROUPS, next_idx, next_dw);
 
@@ -414,15 +401,15 @@ route_backward_kernel(const RouteGradArgs a) {
             int s = seq;
             for (int look = 0; look < 2; ++look) {  // the sequence at hand, else the search
                 if (look) s = find_sequence(a.offsets, a.n_seq, (int)tok);
-                cur_lo = !a.offsets || s < 0 ? 0 : __ldg(a.offsets + s);
-                cur_hi = !a.offsets || s >= a.n_seq ? a.T : __ldg(a.offsets + s + 1);
+                cur_lo = !a.offsets || s < 0 ? 0 : a.offsets[s];
+                cur_hi = !a.offsets || s >= a.n_seq ? a.T : a.offsets[s + 1];
                 if (!a.offsets || ((int)tok >= cur_lo && (int)tok < cur_hi)) break;
             }
             counted = s >= 0 && s < a.n_seq;
             const int s_lo = max(0, cur_lo), len = min(a.T, cur_hi) - s_lo;
             // sum_i p_i = 1, so any constant taken off the counts leaves the
             // gradient as it is; their mean takes the cancellation out of it
-            const double g = counted ? (double)__ldg(a.d_loss + s) * a.alpha /
+            const double g = counted ? (double)a.d_loss[s] * a.alpha /
                                            ((double)a.K * len * len)
                                      : 0.0;
             const int64_t mean = (int64_t)a.K * len;
@@ -431,7 +418,7 @@ route_backward_kernel(const RouteGradArgs a) {
                 const int i = R::expert(glane, q / R::kVec) + q % R::kVec;
                 pull[q] = 0.f;
                 if (counted && i < a.E)
-                    pull[q] = (float)(g * (double)((int64_t)__ldg(a.counts + (size_t)s * a.E + i) *
+                    pull[q] = (float)(g * (double)((int64_t)a.counts[(size_t)s * a.E + i] *
                                                        a.E - mean));
             }
         }
@@ -579,13 +566,10 @@ cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
         auto kern = balance_tile_kernel<decltype(row)>;
         const cudaError_t e = allow_smem(kern, smem);
         if (e != cudaSuccess) return e;
-        kern<<<tiles, BAL_THREADS, smem, st>>>(a);
-        count_launch();
-        return cudaGetLastError();
+        return launch_dependent(kern, tiles, BAL_THREADS, smem, 1, st, a);
     });
     if (err != cudaSuccess || tiles == 1) return err;
-    return launch_dependent(balance_join_kernel, (tiles - 1) * BAL_CLUSTER, BAL_JOIN_THREADS, 0,
-                            BAL_CLUSTER, st, a);
+    return launch_dependent(balance_join_kernel, tiles - 1, BAL_JOIN_THREADS, 0, 1, st, a);
 }
 
 cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
@@ -611,9 +595,8 @@ cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
         // of blocks for long batches, a token a group for short ones
         const int64_t round = (int64_t)groups * grad_blocks<R>() * 148;
         a.tile = (int)((T + round - 1) / round) * groups;
-        kern<<<(unsigned)(((int64_t)T + a.tile - 1) / a.tile), GRAD_THREADS, smem, st>>>(a);
-        count_launch();
-        return cudaGetLastError();
+        return launch_dependent(kern, (unsigned)(((int64_t)T + a.tile - 1) / a.tile), GRAD_THREADS,
+                                smem, 1, st, a);
     });
 }
 

@@ -177,43 +177,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
     const uint32_t smem0 = smem_u32(smem);
     volatile int *abort_flag = &abort_s;
 
-    if (warp == 0) {
-        // tile_base[e] = sum over experts < e of (token tiles x channel blocks)
-        const int nc_r = (p.n_out_r + channels<EPI>() - 1) / channels<EPI>();
-        int carry = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            int lo = 0, cnt = 0;
-            if (e < p.E) {
-                lo = p.offsets[e];
-                const int64_t n = (int64_t)p.offsets[e + 1] - lo;
-                // a segment that leaves the buffer or has a negative length is
-                // treated as empty and reported
-                if (lo < 0 || n < 0 || lo + n > p.rows_r) {
-                    record_status(p.status, MOE_ERR_DEVICE_FAULT);
-                    lo = 0;
-                } else {
-                    cnt = (int)n;
-                }
-                seg[e] = lo;
-                segc[e] = cnt;
-            }
-            const int v = token_tiles(cnt) * nc_r;
-            int incl = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += n;
-            }
-            if (e < p.E) tile_base[e] = carry + incl - v;
-            carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        }
-        if (lane == 0) {
-            tile_base[p.E] = carry;
-            tma_prefetch_desc(&maps.w_r);
-            for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.x_r[i]);
-        }
-    } else if (warp == 1) {
+    if (warp == 1) {
         if (lane == 0) {
             for (int s = 0; s < STAGES; ++s) {
                 mbar_init(smem_u32(&full_bar[s]), 1);
@@ -230,6 +194,48 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         __syncwarp();
         tmem_alloc_pair<TMEM_COLS>(smem_u32(&tmem_base_s));
         tc_fence_before();
+    } else if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.w_r);
+        for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.x_r[i]);
+    }
+    // from here on the kernel reads what the ones before it wrote
+    dependency_wait();
+    dependency_release();
+    for (int e = threadIdx.x; e < p.E; e += NUM_THREADS) {
+        int lo = p.offsets[e], cnt = 0;
+        const int64_t n = (int64_t)p.offsets[e + 1] - lo;
+        // a segment that leaves the buffer or has a negative length is treated as
+        // empty and reported
+        if (lo < 0 || n < 0 || lo + n > p.rows_r) {
+            record_status(p.status, MOE_ERR_DEVICE_FAULT);
+            lo = 0;
+        } else {
+            cnt = (int)n;
+        }
+        seg[e] = lo;
+        segc[e] = cnt;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // tile_base[e] = sum over experts < e of (token tiles x channel blocks): a lane
+        // sums the experts of its share, the warp the shares
+        const int nc_r = (p.n_out_r + channels<EPI>() - 1) / channels<EPI>();
+        const int per = (p.E + 31) / 32;
+        const int e0 = min(p.E, lane * per), e1 = min(p.E, e0 + per);
+        int mine = 0;
+        for (int e = e0; e < e1; ++e) mine += token_tiles(segc[e]) * nc_r;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        int at = incl - mine;
+        for (int e = e0; e < e1; ++e) {
+            tile_base[e] = at;
+            at += token_tiles(segc[e]) * nc_r;
+        }
+        if (lane == 31) tile_base[p.E] = incl;
     }
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are initialised and TMEM is allocated
@@ -356,7 +362,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             const bool shared = t.e < 0;
             const int n_out = shared ? p.n_out_s : p.n_out_r;
             const float *xs_g = (shared ? p.x_scale_s : p.x_scale_r) + t.t0;
-            for (int j = lane; j < t.n; j += 32) xs[j] = j < t.valid ? __ldg(xs_g + j) : 0.f;
+            for (int j = lane; j < t.n; j += 32) xs[j] = j < t.valid ? xs_g[j] : 0.f;
             // this lane's channel (whole warps are inside or outside n_out, a multiple of 64)
             const int ch = EPI == EPI_SWIGLU ? t.c0 + rank * 64 + q * 16 + (lane & 15)
                                              : t.c0 + rank * 128 + q * 32 + lane;
@@ -365,8 +371,8 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             if (ch_ok) {
                 const float *s0 = shared ? p.w0_scale_s : p.w0_scale_r;
                 const float *s1 = shared ? p.w1_scale_s : p.w1_scale_r;
-                ws = __ldg((EPI == EPI_SWIGLU && lane >= 16 ? s1 : s0) +
-                           (size_t)(shared ? 0 : t.e) * n_out + ch);
+                ws = (EPI == EPI_SWIGLU && lane >= 16 ? s1 : s0)[(size_t)(shared ? 0 : t.e) * n_out +
+                                                                 ch];
             }
             __syncwarp();
             if (!mbar_wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, p.status,
@@ -451,24 +457,9 @@ cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t st) {
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_DYN;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     // one wave of pairs, one CTA per SM (pairs that do not fit at once would take
     // their share of the tiles later)
-    cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
-    err = cudaLaunchKernelEx(&cfg, kern, maps, p);
-    count_launch();
-    if (err != cudaSuccess) return err;
-    return cudaGetLastError();
+    return launch_dependent(kern, sm_count() / 2 * 2, NUM_THREADS, SMEM_DYN, 2, st, maps, p);
 }
 
 // Token codes [rows, cols] in boxes of 64, 32 and 16 rows.

@@ -90,6 +90,8 @@ quantize_rows_kernel(const QuantArgs a) {
     constexpr int UNITS = Q_UNITS, Q_THREADS = block_threads<TEAM>();
     const int at = threadIdx.x % TEAM;
     const int64_t row = blockIdx.x * (int64_t)(Q_THREADS / TEAM) + threadIdx.x / TEAM;
+    dependency_wait();
+    dependency_release();
     if (row >= a.rows) return;  // whole teams
     const int per_seg = a.seg_len / U::N, total = JOINT ? per_seg * a.segs : per_seg;
     const int64_t row0 = row * a.row_stride / U::N;  // in 16-byte units from the start of src
@@ -106,7 +108,7 @@ quantize_rows_kernel(const QuantArgs a) {
         for (int k = 0; k < UNITS; ++k) {
             const int u = base + k * TEAM + at;
             v[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (u < total) v[k] = __ldg(src + place(u));
+            if (u < total) v[k] = __ldcg(src + place(u));
         }
 #pragma unroll
         for (int k = 0; k < UNITS; ++k)
@@ -127,7 +129,7 @@ quantize_rows_kernel(const QuantArgs a) {
     if (at == 0 && a.q) a.scale[row] = s;
     if (a.inv_perm)
         for (int j = at; j < a.K; j += TEAM) {
-            const int r = __ldg(a.inv_perm + row * a.K + j);
+            const int r = a.inv_perm[row * a.K + j];
             if (r >= 0 && r < a.n_perm) a.scale_perm[r] = s;
         }
     using Out = typename std::conditional<BF16, uint2, uint32_t>::type;
@@ -138,7 +140,7 @@ quantize_rows_kernel(const QuantArgs a) {
         if (a.q) reinterpret_cast<Out *>(a.q)[row0 + place(u)] = o;
         if (a.inv_perm)
             for (int j = 0; j < a.K; ++j) {
-                const int r = __ldg(a.inv_perm + row * a.K + j);
+                const int r = a.inv_perm[row * a.K + j];
                 if (r >= 0 && r < a.n_perm)
                     reinterpret_cast<Out *>(a.q_perm)[(int64_t)r * total + u] = o;
             }
@@ -155,7 +157,7 @@ quantize_rows_kernel(const QuantArgs a) {
         for (int k = 0; k < UNITS; ++k) {
             const int u = base + k * TEAM + at;
             if (u >= total) continue;
-            if (again) v[k] = __ldg(src + place(u));
+            if (again) v[k] = __ldcg(src + place(u));
             float f[U::N];
 #pragma unroll
             for (int i = 0; i < U::N; ++i) f[i] = U::get(v[k], i);
@@ -169,7 +171,7 @@ quantize_rows_kernel(const QuantArgs a) {
 #pragma unroll 1
         for (; unsure; unsure &= unsure - 1) {
             const int u = base + (__ffs(unsure) - 1) * TEAM + at;
-            const uint4 w = __ldg(src + place(u));
+            const uint4 w = __ldcg(src + place(u));
             uint32_t c[U::N / 4];
 #pragma unroll
             for (int i = 0; i < U::N / 4; ++i) c[i] = 0u;
@@ -187,21 +189,20 @@ cudaError_t run_team(const QuantArgs &a, cudaStream_t st) {
     constexpr int per = block_threads<TEAM>() / TEAM;
     const unsigned grid = (unsigned)((a.rows + per - 1) / per);
     if (BF16 && a.segs > 1)  // the shared experts' down projection; never fp32
-        quantize_rows_kernel<BF16, TEAM, BF16><<<grid, block_threads<TEAM>(), 0, st>>>(a);
-    else
-        quantize_rows_kernel<BF16, TEAM, false><<<grid, block_threads<TEAM>(), 0, st>>>(a);
-    count_launch();
-    return cudaGetLastError();
+        return launch_dependent(quantize_rows_kernel<BF16, TEAM, BF16>, grid, block_threads<TEAM>(),
+                                0, 1, st, a);
+    return launch_dependent(quantize_rows_kernel<BF16, TEAM, false>, grid, block_threads<TEAM>(), 0,
+                            1, st, a);
 }
 
 template <bool BF16>
 cudaError_t run(const QuantArgs &a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
-    constexpr int WIDE = BF16 ? 256 : 512;
     const int64_t lanes = (int64_t)a.segs * a.seg_len / (Unit<BF16>::N * Q_UNITS);
     if (lanes <= 32) return run_team<BF16, 32>(a, st);
     if (lanes <= 128) return run_team<BF16, 128>(a, st);
-    return run_team<BF16, WIDE>(a, st);
+    if (BF16 || lanes <= 256) return run_team<BF16, 256>(a, st);
+    return run_team<BF16, BF16 ? 256 : 512>(a, st);
 }
 
 }  // namespace
