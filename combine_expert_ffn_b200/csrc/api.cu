@@ -1150,7 +1150,8 @@ moe_status check_int8_weights(const moe_config &c, const moe_int8_weights *w) {
 
 cudaError_t ffn_int8(const moe_config &c, const int8_t *x_perm_q, const float *x_scale,
                      const int32_t *offsets, const moe_int8_weights &w, void *y_perm,
-                     void *y_shared, void *ws, const Int8Layout &L, cudaStream_t s) {
+                     void *y_shared, bool after_quantize, void *ws, const Int8Layout &L,
+                     cudaStream_t s) {
     const size_t rows = (size_t)c.T * c.K, ffs = (size_t)c.n_shared * c.d_ff_shared;
     FfnInt8Args a{};
     a.T = c.T; a.d = c.d; a.E = c.E; a.K = c.K; a.d_ff = c.d_ff;
@@ -1166,6 +1167,7 @@ cudaError_t ffn_int8(const moe_config &c, const int8_t *x_perm_q, const float *x
     a.h_shared_q = at<int8_t>(ws, L.base.h_sh);
     a.h_shared_scale = at<float>(ws, L.base.h_sh + (size_t)c.T * ffs);
     a.y_shared = y_shared;
+    a.after_quantize = after_quantize;
     a.status = at<int32_t>(ws, L.base.status);
     a.timeout_ns = kWaitTimeoutNs;
     return launch_expert_ffn_int8(a, s);
@@ -1260,7 +1262,8 @@ moe_status moe_expert_ffn_int8(const moe_config *c, const int8_t *x_perm_q, cons
         launch_quantize_rows_bf16(x, c->T, c->d, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_q_scale),
                                   s))
         return MOE_ERR_CUDA;
-    return cuda_status(ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_shared, ws, L, s));
+    return cuda_status(ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_shared,
+                                c->n_shared > 0, ws, L, s));
 }
 
 moe_status moe_forward_int8(const moe_config *c, const void *x, const float *router_w,
@@ -1322,7 +1325,8 @@ moe_status moe_forward_int8(const moe_config *c, const void *x, const float *rou
                            shared ? at<float>(ws, L8.x_q_scale) : nullptr, s))
         return MOE_ERR_CUDA;
     stage.next("moe.expert_ffn");
-    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, ws, L8, s)) return MOE_ERR_CUDA;
+    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, true, ws, L8, s))
+        return MOE_ERR_CUDA;
     stage.next("moe.combine");
     return cuda_status(launch_combine(y_perm, inv_perm, topk_w, y_sh, c->T, c->d, c->K,
                                       (int64_t)c->T * c->K, out, s));

@@ -76,6 +76,7 @@ struct Params {
     const float *w0_scale_r, *w1_scale_r, *w0_scale_s, *w1_scale_s;
     int gate_r, gate_s;
     void *out_r, *out_s;         // fp32 (SwiGLU) or bf16
+    int early;                   // only the token codes and scales wait for the kernel before
     int32_t *status;
     int64_t timeout_ns;
 };
@@ -198,8 +199,10 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         tma_prefetch_desc(&maps.w_r);
         for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.x_r[i]);
     }
-    // from here on the kernel reads what the ones before it wrote
-    dependency_wait();
+    // From here on the kernel reads what the ones before it wrote.  Where the kernel
+    // right before only writes the token codes and scales, the first weights are
+    // requested while it still runs.
+    if (!p.early) dependency_wait();
     dependency_release();
     for (int e = threadIdx.x; e < p.E; e += NUM_THREADS) {
         int lo = p.offsets[e], cnt = 0;
@@ -266,6 +269,33 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             const int r32 = half & ~63, r16 = half & ~31;
             const uint32_t tx = 2 * (A_BYTES + (uint32_t)half * BK);
             int mat = shared ? 0 : t.e, k = 0, x_col = 0;
+            auto load_weights = [&](int s) {
+                const uint32_t fb = full0 + 8 * s, a_dst = smem0 + s * STAGE_BYTES;
+                if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), tx);
+                if (EPI == EPI_SWIGLU)
+                    tma_load_5d_pair(a_dst, w, fb, k, 0, 0, ch / 16, mat);
+                else
+                    tma_load_3d_pair(a_dst, w, fb, k, ch, mat);
+            };
+            // a run's last block may pass its end: the weights read zeros there
+            auto advance = [&] {
+                k += BK;
+                if (shared && k >= k_len) {
+                    k = 0;
+                    ++mat;
+                    x_col += k_len;
+                }
+            };
+            int ahead = 0;  // k blocks of the first tile whose weights are on their way
+            if (p.early && idx == pair_id) {
+                for (; ahead < min(STAGES, t.kblocks); ++ahead) {
+                    if (elect_one()) load_weights(ahead);
+                    __syncwarp();
+                    advance();
+                }
+                mat = shared ? 0 : t.e, k = 0, x_col = 0;
+                dependency_wait();
+            }
             for (int kb = 0; kb < t.kblocks; ++kb) {
                 if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p)) {
                     ok = false;
@@ -273,30 +303,20 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
                 }
                 if (elect_one()) {
                     const uint32_t fb = full0 + 8 * stage;
-                    const uint32_t a_dst = smem0 + stage * STAGE_BYTES;
-                    const uint32_t b_dst = a_dst + A_BYTES;
-                    if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), tx);
-                    if (EPI == EPI_SWIGLU)
-                        tma_load_5d_pair(a_dst, w, fb, k, 0, 0, ch / 16, mat);
-                    else
-                        tma_load_3d_pair(a_dst, w, fb, k, ch, mat);
+                    const uint32_t b_dst = smem0 + stage * STAGE_BYTES + A_BYTES;
+                    if (kb >= ahead) load_weights(stage);
                     if (half & 16) tma_load_2d_pair(b_dst + r16 * BK, x + 2, fb, x_col + k, tok + r16);
                     if (half & 32) tma_load_2d_pair(b_dst + r32 * BK, x + 1, fb, x_col + k, tok + r32);
                     if (half >= 64) tma_load_2d_pair(b_dst, x, fb, x_col + k, tok);
                     if (half == 128) tma_load_2d_pair(b_dst + 64 * BK, x, fb, x_col + k, tok + 64);
                 }
                 __syncwarp();
-                // a run's last block may pass its end: the weights read zeros there
-                k += BK;
-                if (shared && k >= k_len) {
-                    k = 0;
-                    ++mat;
-                    x_col += k_len;
-                }
+                advance();
                 ++n_issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
+        if (p.early && pair_id >= total) dependency_wait();
         // wind down (leader): every load of both CTAs has landed
         if (leader) {
             for (int s = 0; s < STAGES; ++s) {
@@ -355,6 +375,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int part = (warp - 2) >> 2;
         float *xs = x_scale[warp - 2];
+        if (p.early) dependency_wait();
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int idx = pair_id; idx < total; idx += n_pairs) {
@@ -514,15 +535,13 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
     p.out_s = a.h_shared;
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
+    p.early = a.after_quantize;
     cudaError_t err = launch<EPI_SWIGLU>(m, p, st);
     if (err != cudaSuccess) return err;
 
-    err = launch_quantize_rows_f32(a.h, (int64_t)rows, a.d_ff, a.h_q, a.h_scale, st);
+    err = launch_quantize_rows_f32(a.h, (int64_t)rows, a.d_ff, a.h_q, a.h_scale, a.h_shared,
+                                   has_shared ? a.T : 0, ffs, a.h_shared_q, a.h_shared_scale, st);
     if (err != cudaSuccess) return err;
-    if (has_shared) {
-        err = launch_quantize_rows_f32(a.h_shared, a.T, ffs, a.h_shared_q, a.h_shared_scale, st);
-        if (err != cudaSuccess) return err;
-    }
 
     std::memset(&m, 0, sizeof(m));
     ok = token_maps(m.x_r, a.h_q, rows, a.d_ff) &&
@@ -541,6 +560,7 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
     p.w0_scale_s = p.w1_scale_s = a.w.ws_down_scale;
     p.out_r = a.y_perm;
     p.out_s = a.y_shared;
+    p.early = 1;  // (behind the quantization of h)
     return launch<EPI_STORE>(m, p, st);
 }
 

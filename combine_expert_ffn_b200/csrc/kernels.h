@@ -261,14 +261,15 @@ cudaError_t launch_combine_backward(const void *d_out, const void *y_perm,
                                     cudaStream_t st);
 
 // quant_int8.cu: rows to int8 codes and one fp32 scale each (s = amax / 127,
-// q = rint(x / s)).  bf16 or fp32 rows of `cols` values; rows that run over n_mat
+// q = rint(x / s)).  bf16 rows of `cols` values, or those of two fp32 matrices; rows that run over n_mat
 // matrices [n_mat, rows, cols] with one scale for all of them; and the dispatch
 // gather, codes and scale of token t into the rows inv_perm[t][.] of x_perm_q (and,
 // with x_q, once in token order).
 cudaError_t launch_quantize_rows_bf16(const void *x, int64_t rows, int cols, int8_t *q,
                                       float *scale, cudaStream_t st);
 cudaError_t launch_quantize_rows_f32(const float *x, int64_t rows, int cols, int8_t *q,
-                                     float *scale, cudaStream_t st);
+                                     float *scale, const float *x2, int64_t rows2, int cols2,
+                                     int8_t *q2, float *scale2, cudaStream_t st);
 cudaError_t launch_quantize_joint_bf16(const void *x, int n_mat, int64_t rows, int cols,
                                        int8_t *q, float *scale, cudaStream_t st);
 cudaError_t launch_gather_int8(const void *x, const int32_t *inv_perm, int T, int d, int K,
@@ -292,6 +293,9 @@ struct FfnInt8Args {
     int8_t *h_shared_q;
     float *h_shared_scale;
     void *y_shared;          // [T, d] bf16
+    // the kernel before this call's first (and all before it) has ended when that kernel's
+    // blocks run: offsets and weights may be read before what it writes is there
+    bool after_quantize;
     int32_t *status;
     int64_t timeout_ns;
 };

@@ -31,6 +31,12 @@ struct QuantArgs {
     int64_t n_perm;
     int8_t *q_perm;           // [n_perm, seg_len], one segment only
     float *scale_perm;        // [n_perm]
+    // fp32: a second matrix of one-run rows, worked on by the blocks behind
+    const void *src2;
+    int64_t rows2;
+    int len2;
+    int8_t *q2;
+    float *scale2;
 };
 
 // One 16-byte load: 8 bf16 or 4 fp32 values, as fp32.
@@ -99,13 +105,18 @@ quantize_rows_kernel(const QuantArgs a) {
     using U = Unit<BF16>;
     constexpr int UNITS = Q_UNITS, Q_THREADS = block_threads<TEAM>();
     const int at = threadIdx.x % TEAM;
-    const int64_t row = blockIdx.x * (int64_t)(Q_THREADS / TEAM) + threadIdx.x / TEAM;
+    int64_t row = blockIdx.x * (int64_t)(Q_THREADS / TEAM) + threadIdx.x / TEAM;
     dependency_wait();
     dependency_release();
-    if (row >= a.rows) return;  // whole teams
-    const int per_seg = a.seg_len / U::N, total = JOINT ? per_seg * a.segs : per_seg;
-    const int64_t row0 = row * a.row_stride / U::N;  // in 16-byte units from the start of src
-    const uint4 *src = static_cast<const uint4 *>(a.src) + row0;
+    const bool second = !BF16 && row >= a.rows;
+    if (second) row -= a.rows;
+    if (row >= (second ? a.rows2 : a.rows)) return;  // whole teams
+    const int per_seg = (second ? a.len2 : a.seg_len) / U::N;
+    const int total = JOINT ? per_seg * a.segs : per_seg;
+    // in 16-byte units from the start of src
+    const int64_t row0 = row * ((second ? a.len2 : a.row_stride) / U::N);
+    const uint4 *src = static_cast<const uint4 *>(second ? a.src2 : a.src) + row0;
+    int8_t *const q_out = second ? a.q2 : a.q;
     auto place = [&](int u) {
         if (!JOINT) return (int64_t)u;
         const int seg = u / per_seg;
@@ -144,8 +155,8 @@ quantize_rows_kernel(const QuantArgs a) {
     }
     const float s = top >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu)
                                        : __fdiv_rn(__uint_as_float(top), 127.0f);
-    if (at == 0 && a.q) a.scale[row] = s;
-    if (a.inv_perm)
+    if (at == 0 && q_out) (second ? a.scale2 : a.scale)[row] = s;
+    if (BF16 && a.inv_perm)
         for (int j = at; j < a.K; j += TEAM) {
             const int r = a.inv_perm[row * a.K + j];
             if (r >= 0 && r < a.n_perm) a.scale_perm[r] = s;
@@ -155,8 +166,8 @@ quantize_rows_kernel(const QuantArgs a) {
         Out o;
         if constexpr (BF16) o = make_uint2(c[0], c[1]);
         else o = c[0];
-        if (a.q) reinterpret_cast<Out *>(a.q)[row0 + place(u)] = o;
-        if (a.inv_perm)
+        if (q_out) reinterpret_cast<Out *>(q_out)[row0 + place(u)] = o;
+        if (BF16 && a.inv_perm)
             for (int j = 0; j < a.K; ++j) {
                 const int r = a.inv_perm[row * a.K + j];
                 if (r >= 0 && r < a.n_perm)
@@ -205,7 +216,7 @@ quantize_rows_kernel(const QuantArgs a) {
 template <bool BF16, int TEAM>
 cudaError_t run_team(const QuantArgs &a, cudaStream_t st) {
     constexpr int per = block_threads<TEAM>() / TEAM;
-    const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+    const unsigned grid = (unsigned)((a.rows + a.rows2 + per - 1) / per);
     if (BF16 && a.segs > 1)  // the shared experts' down projection; never fp32
         return launch_dependent(quantize_rows_kernel<BF16, TEAM, BF16>, grid, block_threads<TEAM>(),
                                 0, 1, st, a);
@@ -215,7 +226,7 @@ cudaError_t run_team(const QuantArgs &a, cudaStream_t st) {
 
 template <bool BF16>
 cudaError_t run(const QuantArgs &a, cudaStream_t st) {
-    if (a.rows == 0) return cudaSuccess;
+    if (a.rows + a.rows2 == 0) return cudaSuccess;
     const int64_t lanes = (int64_t)a.segs * a.seg_len / (Unit<BF16>::N * Q_UNITS);
     if (lanes <= 32) return run_team<BF16, 32>(a, st);
     if (lanes <= 128) return run_team<BF16, 128>(a, st);
@@ -234,10 +245,23 @@ cudaError_t launch_quantize_rows_bf16(const void *x, int64_t rows, int cols, int
 }
 
 cudaError_t launch_quantize_rows_f32(const float *x, int64_t rows, int cols, int8_t *q,
-                                     float *scale, cudaStream_t st) {
+                                     float *scale, const float *x2, int64_t rows2, int cols2,
+                                     int8_t *q2, float *scale2, cudaStream_t st) {
     QuantArgs a{};
     a.src = x; a.rows = rows; a.segs = 1; a.seg_len = cols; a.row_stride = cols;
     a.q = q; a.scale = scale;
+    QuantArgs b{};
+    b.src = x2; b.rows = rows2; b.segs = 1; b.seg_len = cols2; b.row_stride = cols2;
+    b.q = q2; b.scale = scale2;
+    // one launch where both take the same number of lanes a row (a launch saved is 2 us
+    // of a single token's 84)
+    auto lanes = [](int c) { return c <= 512 ? 32 : c <= 2048 ? 128 : c <= 4096 ? 256 : 512; };
+    if (rows2 > 0 && lanes(cols) != lanes(cols2)) {
+        const cudaError_t err = run<false>(b, st);
+        if (err != cudaSuccess) return err;
+    } else {
+        a.src2 = x2; a.rows2 = rows2; a.len2 = cols2; a.q2 = q2; a.scale2 = scale2;
+    }
     return run<false>(a, st);
 }
 
