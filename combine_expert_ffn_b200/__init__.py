@@ -237,10 +237,12 @@ class _Call:
     def t(self, t, dtype, numel):
         if t is None or isinstance(t, int):
             return t
-        if t.dtype is dtype and t.is_contiguous() and t.numel() >= numel and t.is_cuda:
-            if self.dev is None:
-                self.dev = torch.cuda.current_device()
-            if t.get_device() == self.dev:
+        if t.dtype is dtype and t.numel() >= numel and t.is_contiguous():
+            dev = t.get_device()  # -1 on the host
+            if dev == self.dev:
+                return t.data_ptr()
+            if dev >= 0 and self.dev is None and dev == torch.cuda.current_device():
+                self.dev = dev
                 return t.data_ptr()
         raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
 
