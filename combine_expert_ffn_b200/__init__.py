@@ -246,6 +246,14 @@ class _Call:
                 return t.data_ptr()
         raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
 
+    def ws(self, ws):
+        """(device pointer, bytes) of a workspace tensor."""
+        if ws is None:
+            return None, 0
+        if ws.get_device() != torch.cuda.current_device():
+            raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
     def sequences(self, seq_offsets):
         """(device pointer, number of sequences) of a seq_offsets argument."""
         if seq_offsets is None:
@@ -375,10 +383,9 @@ def moe_balance_loss(cfg, scores, topk_idx, seq_offsets, alpha, counts, prob, lo
     k = _Call("moe_balance_loss", cfg)
     c, t, f32, i32 = k.c, k.t, torch.float32, torch.int32
     seq, n = k.sequences(seq_offsets)
-    wp, wn = _ws(ws)
     _ok(k.fn, _lib.moe_balance_loss(
         C.byref(c), t(scores, f32, c.T * c.E), t(topk_idx, i32, c.T * c.K), seq, n, alpha,
-        t(counts, i32, n * c.E), t(prob, f32, n * c.E), t(loss, f32, n), wp, wn,
+        t(counts, i32, n * c.E), t(prob, f32, n * c.E), t(loss, f32, n), *k.ws(ws),
         k.stream(stream)))
 
 
@@ -458,13 +465,12 @@ def moe_dispatch_int8(cfg, x, topk_idx, counts, offsets, send, send_tok, perm_to
                       x_perm_q, x_scale, ws, stream=None) -> None:
     k = _Call("moe_dispatch_int8", cfg)
     c, t, i32 = k.c, k.t, torch.int32
-    wp, wn = _ws(ws)
     rows, groups = c.T * c.K, c.G * c.G
     _ok(k.fn, _lib.moe_dispatch_int8(
         C.byref(c), t(x, torch.bfloat16, c.T * c.d), t(topk_idx, i32, rows), t(counts, i32, c.E),
         t(offsets, i32, c.E + 1), t(send, i32, groups), t(send_tok, i32, groups),
         t(perm_token, i32, rows), t(inv_perm, i32, rows), t(x_perm_q, torch.int8, rows * c.d),
-        t(x_scale, torch.float32, rows), wp, wn, k.stream(stream)))
+        t(x_scale, torch.float32, rows), *k.ws(ws), k.stream(stream)))
 
 
 def moe_expert_ffn_int8(cfg, x_perm_q, x_scale, offsets, weights, y_perm, x, y_shared, ws,
@@ -472,13 +478,12 @@ def moe_expert_ffn_int8(cfg, x_perm_q, x_scale, offsets, weights, y_perm, x, y_s
     """weights: Int8Weights."""
     k = _Call("moe_expert_ffn_int8", cfg)
     c, t, bf16 = k.c, k.t, torch.bfloat16
-    wp, wn = _ws(ws)
     rows = c.T * c.K
     weights.check(k.fn, c)
     _ok(k.fn, _lib.moe_expert_ffn_int8(
         C.byref(c), t(x_perm_q, torch.int8, rows * c.d), t(x_scale, torch.float32, rows),
         t(offsets, torch.int32, c.E + 1), C.byref(weights), t(y_perm, bf16, rows * c.d),
-        t(x, bf16, c.T * c.d), t(y_shared, bf16, c.T * c.d), wp, wn, k.stream(stream)))
+        t(x, bf16, c.T * c.d), t(y_shared, bf16, c.T * c.d), *k.ws(ws), k.stream(stream)))
 
 
 def moe_forward_int8(cfg, x, router_w, logit_offset, bias, weights, out, topk_idx=None,
@@ -487,7 +492,6 @@ def moe_forward_int8(cfg, x, router_w, logit_offset, bias, weights, out, topk_id
     """weights: Int8Weights; ws: alloc_int8_workspace(cfg)."""
     k = _Call("moe_forward_int8", cfg)
     c, t, i32, f32 = k.c, k.t, torch.int32, torch.float32
-    wp, wn = _ws(ws)
     rows, groups = c.T * c.K, c.G * c.G
     weights.check(k.fn, c)
     _ok(k.fn, _lib.moe_forward_int8(
@@ -495,7 +499,7 @@ def moe_forward_int8(cfg, x, router_w, logit_offset, bias, weights, out, topk_id
         t(logit_offset, f32, c.E), t(bias, f32, c.E), t(token_ids, torch.int64, c.T),
         C.byref(weights), t(out, torch.bfloat16, c.T * c.d), t(topk_idx, i32, rows),
         t(topk_w, f32, rows), t(counts, i32, c.E), t(offsets, i32, c.E + 1),
-        t(send, i32, groups), t(send_tok, i32, groups), wp, wn, k.stream(stream)))
+        t(send, i32, groups), t(send_tok, i32, groups), *k.ws(ws), k.stream(stream)))
 
 
 # ----------------------------------------------------------------- expert parallelism

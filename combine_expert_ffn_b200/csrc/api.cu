@@ -1135,6 +1135,12 @@ bool int8_lengths_ok(const moe_config &c) {
     return c.d < 131072 && c.d_ff < 131072 && (int64_t)c.n_shared * c.d_ff_shared < 131072;
 }
 
+// One tensor map spans both matrices: the step between them is one of its strides.
+bool gate_up_pair(const void *gate, const void *up) {
+    const uintptr_t g = reinterpret_cast<uintptr_t>(gate), u = reinterpret_cast<uintptr_t>(up);
+    return g != u && (g < u ? u - g : g - u) < (uintptr_t{1} << 40);
+}
+
 moe_status check_int8_weights(const moe_config &c, const moe_int8_weights *w) {
     if (!w) return MOE_ERR_INVALID_ARG;
     const void *routed[] = {w->w_gate, w->w_up, w->w_down, w->w_gate_scale, w->w_up_scale,
@@ -1145,6 +1151,8 @@ moe_status check_int8_weights(const moe_config &c, const moe_int8_weights *w) {
         if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
     for (const void *p : shared)
         if (c.n_shared > 0 && (!p || !aligned16(p))) return MOE_ERR_INVALID_ARG;
+    if (!gate_up_pair(w->w_gate, w->w_up)) return MOE_ERR_INVALID_ARG;
+    if (c.n_shared > 0 && !gate_up_pair(w->ws_gate, w->ws_up)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 

@@ -24,6 +24,9 @@
  *             Implemented: shared + fine-grained routed experts).
  *   combine   out_t = shared_t + sum_j w_j y_(t,j) back in token order (the
  *             combine all-to-all, same section).
+ * Training: the balance loss and the gradients of the router and of the combine
+ * (moe_balance_loss, moe_route_backward, moe_combine_backward).  Serving in fewer
+ * bits: dispatch, experts and layer in int8 (moe_forward_int8 and its stages).
  * Variants (same passage of Exp08, Implemented): the V4 affinity
  * sqrt(softplus(L)) in place of the sigmoid, a hash router for early layers,
  * and the per-expert bias update that balances the load without an
@@ -511,7 +514,9 @@ MOE_API moe_status moe_forward_packed(const moe_config *cfg, const void *x, cons
  *   ws_gate, ws_up [n_shared, d_ff_shared, d], ..._scale [n_shared, d_ff_shared]
  *   ws_down      [n_shared, d, d_ff_shared], ws_down_scale [d]: one scale per
  *                channel for all shared experts, whose outputs are one sum
- * (the six ws_ pointers may be NULL when n_shared == 0).
+ * (the six ws_ pointers may be NULL when n_shared == 0).  w_gate and w_up are two
+ * buffers less than 2^40 bytes apart, and so are ws_gate and ws_up
+ * (MOE_ERR_INVALID_ARG otherwise).
  */
 typedef struct moe_int8_weights {
     int8_t *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;

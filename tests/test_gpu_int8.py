@@ -196,6 +196,53 @@ def test_integer_sums_are_exact():
     assert ((y.double() - want).abs() <= (2.0 ** -8 + 2 * R.H_REL) * want.abs()).all()
 
 
+def test_gate_and_up_in_either_order_of_addresses():
+    cfg, xq, xs, offsets, w, x = ffn_inputs((90, 192, 3, 2, 192, 2, 64, 0.0))
+    y, sh, _ = run_ffn(cfg, xq, xs, offsets, w, x)
+    for first, second in (("gate", "up"), ("up", "gate")):
+        v = dict(w)
+        for k in ("w_", "ws_"):
+            both = torch.stack([w[k + first], w[k + second]])
+            v[k + first], v[k + second] = both[0], both[1]
+        y2, sh2, _ = run_ffn(cfg, xq, xs, offsets, v, x)
+        assert torch.equal(y, y2) and torch.equal(sh, sh2)
+    check_ffn(cfg, xq, xs, offsets, w, x, y, sh)
+
+
+def test_rows_behind_the_2_to_the_31st_byte():
+    """Dispatch, experts and the combine's gradient at 300,032 rows of 7168: codes pass 2^31 bytes,
+    bf16 rows 2^32.  The last rows against their definition, the dispatch in full."""
+    T, d, E, K, d_ff = 37504, 7168, 8, 8, 64
+    cfg, g = config(T, d, E, K, d_ff), gen(9)
+    x = torch.randn(T, d, device=DEV, generator=g).bfloat16()
+    idx = torch.rand(T, E, device=DEV, generator=g).argsort(1).int()
+    ws = moe.alloc_int8_workspace(cfg)
+    o, q, s = dispatch(cfg, x, idx, ws)
+    rq, rs = R.quantize(x.float())
+    rq = rq.to(torch.int8)
+    for rows in torch.arange(T * K, device=DEV).split(50000):
+        tok = o["perm_token"][rows].long()
+        assert torch.equal(q[rows], rq[tok]) and torch.equal(s[rows].double(), rs[tok, 0])
+    w = random_weights(cfg, g)
+    y, _, _ = run_ffn(cfg, q, s, o["offsets"], w, x, ws)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    tail = 200
+    last = {k: v[E - 1:] for k, v in w.items()}
+    seg = torch.tensor([0, tail], dtype=torch.int32)
+    check_ffn(cfg, q[-tail:], s[-tail:], seg, last, None, y[-tail:], None)
+    up = torch.randn(T, d, device=DEV, generator=g).bfloat16()
+    gate = torch.rand(T, K, device=DEV, generator=g)
+    dy, dw = torch.empty_like(y), torch.empty(T, K, device=DEV)
+    moe.moe_combine_backward(cfg, up, y, o["inv_perm"], gate, dy, dw)
+    t = torch.arange(T - 50, T, device=DEV)
+    rows = o["inv_perm"][t].long()
+    want = gate[t].double()[:, :, None] * up[t].double()[:, None]
+    assert ((dy[rows].double() - want).abs() <= (2.0 ** -8 + 2 * R.U) * want.abs()).all()
+    prod = up[t].double()[:, None] * y[rows].double()
+    n = 8 * -(-d // 256) + 13
+    assert ((dw[t].double() - prod.sum(2)).abs() <= n * R.U * prod.abs().sum(2)).all()
+
+
 def test_a_row_with_a_nan_scale_is_nan_and_no_other():
     cfg, xq, xs, offsets, w, x = ffn_inputs((70, 128, 4, 2, 192, 1, 64, 0.0))
     y, sh, _ = run_ffn(cfg, xq, xs, offsets, w, x)

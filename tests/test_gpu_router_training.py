@@ -288,6 +288,64 @@ def test_route_backward_bad_and_repeated_ids():
     assert ((out.double() - ref).abs() <= 2 * route_bound(s, twice, dw, zero, 0) + 1e-30).all()
 
 
+@pytest.mark.parametrize("T,E,K", [(40, 24, 12), (33, 256, 17), (20, 30, 9)])
+def test_route_backward_repeated_ids_in_long_choices(T, E, K):
+    """Two gates of one expert where a lane holds several of a token's gates."""
+    cfg = cfg_of(T, E, K)
+    s, idx, g = inputs(T, E, K)
+    idx = idx.clone()
+    idx[:, K - 1] = idx[:, 0]
+    dw = torch.randn(T, K, device=DEV, generator=g)
+    out = torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(cfg, s, idx, dw, None, None, None, 0.0, out)
+    ref = reference(s, idx, dw, None, None, None, 0.0, 0)
+    zero = torch.zeros(T, E, dtype=torch.float64, device=DEV)
+    assert ((out.double() - ref).abs() <= 2 * route_bound(s, idx, dw, zero, 0)).all()
+
+
+def test_more_affinities_than_2_to_the_31():
+    T, E, K = (1 << 21) + 37, 1024, 2
+    cfg, alpha = cfg_of(T, E, K), 1.0
+    g = torch.Generator(device=DEV).manual_seed(11)
+    s = torch.rand(T, E, device=DEV, generator=g) * 0.9 + 0.05
+    a = torch.randint(0, E, (T,), device=DEV, generator=g)
+    idx = torch.stack([a, (a + 1 + a % 7) % E], 1).int()
+    cut = T - 300
+    o = [0, 1000, cut, T]
+    n, p, loss, ws = balance(cfg, s, idx, offsets(o), alpha)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    assert torch.equal(n.long(), R.counts(idx, o, E))
+    tail = R.balance_loss(s[cut:].double(), n[2:], [0, 300], alpha, K)
+    assert ((p[2].double() - tail[0][0]).abs() <= 200 * U * tail[0][0]).all()
+    assert abs(float(loss[2]) - float(tail[1][0])) <= 204 * U * float(tail[1][0])
+    # the long sequence's shares add up to 1, each within its own relative error
+    bound = (40 + tile(T) / 16 + 2 + 17 + T / tile(T) / 8 + 9) * U
+    assert abs(float(p[1].double().sum()) - 1) <= bound
+    dl = torch.tensor([1.0, 1.0, 300.0], device=DEV)
+    dw = torch.randn(T, K, device=DEV, generator=g)
+    out = torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(cfg, s, idx, dw, offsets(o), n, dl, alpha, out)
+    sub, o2 = slice(cut, T), [0, 300]
+    ref = reference(s[sub], idx[sub], dw[sub], o2, n[2:].long(), dl[2:], alpha, 0)
+    pull = pull_of(n[2:], o2, dl[2:], alpha, K, 300, E)
+    assert ((out[sub].double() - ref).abs() <= route_bound(s[sub], idx[sub], dw[sub], pull, 0)).all()
+
+
+def test_many_short_sequences():
+    """Every token a sequence of its own, more of them than one tile's search probes at once."""
+    T, E, K = 20000, 24, 3
+    cfg = cfg_of(T, E, K)
+    s, idx, _ = inputs(T, E, K)
+    o = list(range(0, T + 1))
+    n, p, loss, _ = balance(cfg, s, idx, offsets(o), 1.0)
+    want = torch.zeros(T, E, device=DEV).scatter_(1, idx.long(), 1.0)
+    assert torch.equal(n.float(), want)
+    share = s.double() / s.double().sum(1, keepdim=True)
+    assert ((p.double() - share).abs() <= 60 * U * share).all()
+    ref = (share * want.double()).sum(1) * E / K
+    assert ((loss.double() - ref).abs() <= 64 * U * ref).all()
+
+
 # ------------------------------------------------------------------ combine gradient
 COMBINE = [(1, 64, 1), (1, 7168, 8), (3, 320, 5), (40, 128, 32), (300, 2048, 6), (700, 576, 8),
            (2500, 64, 1), (9, 8256, 3)]

@@ -99,7 +99,7 @@ def test_combine_backward_arguments(moe):
 def weights(moe, **kw):
     w = moe.Int8Weights()
     for n, _ in w._fields_:
-        setattr(w, n, kw.get(n, P))
+        setattr(w, n, kw.get(n, P + 4096 * (n in ("w_up", "ws_up"))))
     return w
 
 
@@ -174,6 +174,10 @@ def test_expert_ffn_int8_arguments(moe):
     for f, _ in moe.Int8Weights._fields_:
         for bad in (None, P + 4):
             assert call(w=weights(moe, **{f: bad})) == moe.MOE_ERR_INVALID_ARG, f
+    for pair in ("w", "ws"):  # gate and up: two buffers, less than 2^40 bytes apart
+        for gate, up in ((P, P), (P, P + (1 << 40)), (P + (1 << 40), P)):
+            assert call(w=weights(moe, **{pair + "_gate": gate, pair + "_up": up})) == \
+                moe.MOE_ERR_INVALID_ARG
     assert call(wn=n - 1) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
     assert call(wn=moe.moe_workspace_size(c)) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
     assert call(c=cfg(moe, d=131072)) == moe.MOE_ERR_UNSUPPORTED_SHAPE
