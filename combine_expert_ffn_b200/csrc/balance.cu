@@ -29,6 +29,8 @@
 // order; a sequence that crosses tiles leaves one partial row per tile, which a
 // second kernel adds in tile order.  No float atomics: equal inputs give equal
 // bits.
+#include <climits>
+
 #include "kernels.h"
 
 namespace moe {
@@ -198,11 +200,20 @@ balance_tile_kernel(const BalanceArgs a) {
         const int end = min(hi_tile, s_hi);
         for (int i = threadIdx.x; i < a.E; i += BAL_THREADS) hist[i] = 0;
         __syncthreads();
-        for (int64_t c = (int64_t)t * a.K + threadIdx.x; c < (int64_t)end * a.K;
-             c += BAL_THREADS) {
-            const int i = a.topk_idx[c];
-            if (i >= 0 && i < a.E) atomicAdd(hist + i, 1);
-            else record_status(a.status, MOE_ERR_DEVICE_FAULT);
+        // ids in batches whose loads are in flight together (one by one they took 6 us of
+        // the 58 of 262144 tokens)
+        constexpr int BATCH = 8;
+        const int64_t last_id = (int64_t)end * a.K;
+        for (int64_t c = (int64_t)t * a.K + threadIdx.x; c < last_id; c += BATCH * BAL_THREADS) {
+            int id[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                id[k] = c + k * BAL_THREADS < last_id ? a.topk_idx[c + k * BAL_THREADS] : INT_MIN;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (id[k] >= 0 && id[k] < a.E) atomicAdd(hist + id[k], 1);
+                else if (c + k * BAL_THREADS < last_id) record_status(a.status, MOE_ERR_DEVICE_FAULT);
+            }
         }
         float acc[NV], v[NV];
 #pragma unroll
