@@ -198,6 +198,8 @@ balance_tile_kernel(const BalanceArgs a) {
             sequence_range(a.offsets, s, a.T, &s_lo, &s_hi);
         }
         const int end = min(hi_tile, s_hi);
+        float v[NV];  // the first rows come in beside the ids
+        R::load(a.scores, t + group, end, glane, a.E, v);
         for (int i = threadIdx.x; i < a.E; i += BAL_THREADS) hist[i] = 0;
         __syncthreads();
         // ids in batches whose loads are in flight together (one by one they took 6 us of
@@ -215,10 +217,9 @@ balance_tile_kernel(const BalanceArgs a) {
                 else if (c + k * BAL_THREADS < last_id) record_status(a.status, MOE_ERR_DEVICE_FAULT);
             }
         }
-        float acc[NV], v[NV];
+        float acc[NV];
 #pragma unroll
         for (int q = 0; q < NV; ++q) acc[q] = 0.f;
-        R::load(a.scores, t + group, end, glane, a.E, v);
         // whole warps stay in the loop: the sums are shuffles
         for (uint32_t u = t; u < (uint32_t)end; u += GROUPS) {
             float next[NV];
