@@ -98,8 +98,10 @@ cudaError_t launch_combine(const void *y_perm, const int32_t *inv_perm, const fl
 //   d_y_perm[row(t,j)] = bf16(w_(t,j) d_out[t]),  d_topk_w[t][j] = d_out[t] . y_perm[row(t,j)]
 // (y_shared's gradient is d_out itself.)  HBM-bound: per copy one row read and
 // one written, and d_out once per token: the K warps of a token run side by
-// side in a block, so that K - 1 of them find its row in L1.  WARPS warps share
-// a copy's row: one when the copies fill the GPU, eight for short batches.
+// side in a block, so that K - 1 of them find its row in L1.  8192 tokens of 7168
+// with K = 8 take 326 us, 6.1 TB/s of the 1.99 GB.  WARPS warps share a copy's
+// row: one, which has no sum across warps to wait for, or, for few or long rows,
+// eight, whose loads are all in flight at once.
 template <int WARPS, bool DY, bool DW>
 __global__ void __launch_bounds__(CB_THREADS)
 combine_backward_kernel(const uint4 *__restrict__ d_out, const uint4 *__restrict__ y_perm,
@@ -145,18 +147,19 @@ combine_backward_kernel(const uint4 *__restrict__ d_out, const uint4 *__restrict
             }
         }
     }
-    if (!DW) return;
+    if constexpr (DW) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-    if (WARPS > 1) {
-        __shared__ float part[CB_THREADS / 32];
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-        __syncthreads();
-        dot = 0.f;
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        if (WARPS > 1) {
+            __shared__ float part[CB_THREADS / 32];
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+            __syncthreads();
+            dot = 0.f;
 #pragma unroll
-        for (int k = 0; k < WARPS; ++k) dot += part[k];
+            for (int k = 0; k < WARPS; ++k) dot += part[k];
+        }
+        if (at == 0) d_topk_w[copy] = dot;
     }
-    if (at == 0) d_topk_w[copy] = dot;
 }
 
 namespace {
@@ -185,10 +188,13 @@ cudaError_t launch_combine_backward(const void *d_out, const void *y_perm,
     if (T == 0 || (!d_y_perm && !d_topk_w)) return cudaSuccess;
     const uint4 *g = static_cast<const uint4 *>(d_out), *y = static_cast<const uint4 *>(y_perm);
     uint4 *dy = static_cast<uint4 *>(d_y_perm);
-    if (n_rows >= 148 * 16)
-        run_combine_backward<1>(g, y, inv_perm, topk_w, d / 8, K, n_rows, dy, d_topk_w, st);
-    else
+    // Eight warps a row and one, in us, by d and copies: 2048: 256 2.5 and 3.5, 512 3.4 and
+    // 3.6, 1024 4.9 and 3.7; 4096: 1024 5.7 and 6.9, 8192 38 and 28; 7168: 1024 7.2 and 12.6,
+    // 8192 47 and 50, 65536 363 and 325.  The crossing grows as d^2.
+    if (n_rows * 8192 <= (int64_t)d * d)
         run_combine_backward<8>(g, y, inv_perm, topk_w, d / 8, K, n_rows, dy, d_topk_w, st);
+    else
+        run_combine_backward<1>(g, y, inv_perm, topk_w, d / 8, K, n_rows, dy, d_topk_w, st);
     count_launch();
     return cudaGetLastError();
 }

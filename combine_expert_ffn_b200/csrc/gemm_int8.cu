@@ -31,8 +31,20 @@
 //   GEMM2  256 channels; pairs of lanes exchange one of two tokens so that each
 //          stores two neighbouring channels of one
 // One persistent kernel per GEMM, 320 threads a CTA: warp 0 the TMA producer, warp
-// 1 (of the leading CTA) the MMA issuer, warps 2..9 the epilogue.  Rows of a tile
-// past its segment are computed and never stored.  Every wait is bounded.
+// 1 (of the leading CTA) the MMA issuer, warps 2..9 the epilogue.  Producer and issuer
+// are converged warps of which one elected lane issues: under a test of the lane number
+// each TMA and MMA instruction loops over the lanes, and a k block took 340 ns to issue
+// where its products take 270.  Rows of a tile past its segment are computed and never
+// stored.  Every wait on a barrier is bounded.
+//
+// Measured with d = 7168, 256 experts of d_ff 2048, K = 8 and one shared expert:
+//   128 tokens   1.69 ms for 11.2 GB, 6.6 TB/s: HBM bounds it
+//   1 token      78 us for 0.40 GB, 5.1 TB/s: the first loads of each GEMM and the last,
+//                partly filled round of tiles (252 of GEMM2 over 74 pairs)
+//   8192 tokens  4.1 ms, 1.6 POP/s: the power limit.  Back to back passes run at 1.05 to
+//                1.1 GHz; the first ones, at up to 1.9 GHz, take 3.3 ms.  The products
+//                alone (no loads, no epilogue) would take 2.3 ms at the same power, the
+//                token loads cost 0.7, the weight loads 1.4, epilogue and h 0.6 ms
 #include <cstring>
 
 #include "kernels.h"
