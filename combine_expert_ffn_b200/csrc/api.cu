@@ -1236,11 +1236,10 @@ moe_status moe_dispatch_int8(const moe_config *c, const void *x, const int32_t *
     cudaStream_t s = as_stream(stream);
     DispatchWs dw{at<int32_t>(ws, L.hist_t), at<int32_t>(ws, L.base_t),
                   at<int32_t>(ws, L.send_part), at<int32_t>(ws, L.sendtok_part)};
-    if (launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send, send_tok,
-                        perm_token, inv_perm, nullptr, dw, at<int32_t>(ws, L.status), s))
-        return MOE_ERR_CUDA;
-    return cuda_status(launch_gather_int8(x, inv_perm, c->T, c->d, c->K, x_perm_q, x_scale, nullptr,
-                                          nullptr, s));
+    return cuda_status(launch_dispatch_int8(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts,
+                                            offsets, send, send_tok, perm_token, inv_perm, x_perm_q,
+                                            x_scale, nullptr, nullptr, dw,
+                                            at<int32_t>(ws, L.status), s));
 }
 
 moe_status moe_expert_ffn_int8(const moe_config *c, const int8_t *x_perm_q, const float *x_scale,
@@ -1326,14 +1325,16 @@ moe_status moe_forward_int8(const moe_config *c, const void *x, const float *rou
     int8_t *x_perm_q = at<int8_t>(ws, L.x_perm);
     float *x_scale = at<float>(ws, L.x_perm + (size_t)c->T * c->K * c->d);
     const bool shared = c->n_shared > 0;
-    if (launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send, send_tok,
-                        perm_token, inv_perm, nullptr, dw, at<int32_t>(ws, L.status), s) ||
-        launch_gather_int8(x, inv_perm, c->T, c->d, c->K, x_perm_q, x_scale,
-                           shared ? at<int8_t>(ws, L8.x_q) : nullptr,
-                           shared ? at<float>(ws, L8.x_q_scale) : nullptr, s))
+    if (launch_dispatch_int8(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send,
+                             send_tok, perm_token, inv_perm, x_perm_q, x_scale,
+                             shared ? at<int8_t>(ws, L8.x_q) : nullptr,
+                             shared ? at<float>(ws, L8.x_q_scale) : nullptr, dw,
+                             at<int32_t>(ws, L.status), s))
         return MOE_ERR_CUDA;
     stage.next("moe.expert_ffn");
-    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, true, ws, L8, s))
+    // (the one-kernel dispatch also writes the offsets: nothing may be read ahead of it)
+    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, !dispatch_int8_in_one(c->T), ws, L8,
+                 s))
         return MOE_ERR_CUDA;
     stage.next("moe.combine");
     return cuda_status(launch_combine(y_perm, inv_perm, topk_w, y_sh, c->T, c->d, c->K,

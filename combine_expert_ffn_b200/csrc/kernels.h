@@ -262,9 +262,9 @@ cudaError_t launch_combine_backward(const void *d_out, const void *y_perm,
 
 // quant_int8.cu: rows to int8 codes and one fp32 scale each (s = amax / 127,
 // q = rint(x / s)).  bf16 rows of `cols` values, or those of two fp32 matrices; rows that run over n_mat
-// matrices [n_mat, rows, cols] with one scale for all of them; and the dispatch
-// gather, codes and scale of token t into the rows inv_perm[t][.] of x_perm_q (and,
-// with x_q, once in token order).
+// matrices [n_mat, rows, cols] with one scale for all of them; and the dispatch,
+// codes and scale of token t into the rows inv_perm[t][.] of x_perm_q (and, with
+// x_q, once in token order).
 cudaError_t launch_quantize_rows_bf16(const void *x, int64_t rows, int cols, int8_t *q,
                                       float *scale, cudaStream_t st);
 cudaError_t launch_quantize_rows_f32(const float *x, int64_t rows, int cols, int8_t *q,
@@ -272,9 +272,14 @@ cudaError_t launch_quantize_rows_f32(const float *x, int64_t rows, int cols, int
                                      int8_t *q2, float *scale2, cudaStream_t st);
 cudaError_t launch_quantize_joint_bf16(const void *x, int n_mat, int64_t rows, int cols,
                                        int8_t *q, float *scale, cudaStream_t st);
-cudaError_t launch_gather_int8(const void *x, const int32_t *inv_perm, int T, int d, int K,
-                               int8_t *x_perm_q, float *x_scale, int8_t *x_q, float *x_q_scale,
-                               cudaStream_t st);
+// The dispatch with int8 rows; one kernel for batches of one dispatch block, which
+// then writes offsets, else the plan of dispatch.cu and the gather behind it.
+inline bool dispatch_int8_in_one(int T) { return T > 0 && T <= DISPATCH_BLOCK; }
+cudaError_t launch_dispatch_int8(const void *x, const int32_t *topk_idx, int T, int d, int E, int G,
+                                 int K, int32_t *counts, int32_t *offsets, int32_t *send,
+                                 int32_t *send_tok, int32_t *perm_token, int32_t *inv_perm,
+                                 int8_t *x_perm_q, float *x_scale, int8_t *x_q, float *x_q_scale,
+                                 const DispatchWs &ws, int32_t *status, cudaStream_t st);
 
 // gemm_int8.cu: the expert FFN on int8 codes (see moe_expert_ffn_int8)
 struct FfnInt8Args {

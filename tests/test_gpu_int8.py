@@ -89,6 +89,37 @@ def test_dispatch_int8(T, d, E, K):
     assert moe.moe_read_device_status(ws) == moe.MOE_OK
 
 
+@pytest.mark.parametrize("T,d,E,G,K,M", [(4, 64, 16, 4, 4, 2), (64, 128, 16, 4, 4, 2),
+                                         (256, 192, 256, 8, 8, 4), (256, 64, 1024, 64, 32, 32),
+                                         (255, 8256, 40, 5, 6, 2), (257, 320, 12, 1, 4, 1),
+                                         (264, 320, 12, 4, 4, 2), (1, 64, 1, 1, 1, 1)])
+@pytest.mark.parametrize("bad", [False, True])
+def test_dispatch_int8_plan_is_moe_dispatchs(T, d, E, G, K, M, bad):
+    """Every output of the plan, in batches of one launch (up to 256 tokens) and of several; with
+    ids out of range and an expert listed twice too, which are flagged and skipped alike."""
+    cfg, g = config(T, d, E, K, 64, G=G, M=M), gen(T + E)
+    x = torch.randn(T, d, device=DEV, generator=g).bfloat16()
+    idx = routing(T, E, K, g, 1.0)
+    if bad:
+        idx[T // 2, 0] = E
+        idx[T - 1, K - 1] = -7
+        if K > 1:
+            idx[0, 1] = idx[0, 0]
+    ws = moe.alloc_workspace(cfg)
+    o, q, s = dispatch(cfg, x, idx, ws)
+    assert moe.moe_read_device_status(ws) == (moe.MOE_ERR_DEVICE_FAULT if bad else moe.MOE_OK)
+    plain = {k: torch.full_like(v, -3) for k, v in o.items()}
+    moe.moe_dispatch(cfg, None, idx, *plain.values(), None, moe.alloc_workspace(cfg))
+    n = int(plain["offsets"][-1])
+    for k in o:
+        a, b = (o[k][:n], plain[k][:n]) if k == "perm_token" else (o[k], plain[k])
+        assert torch.equal(a, b), k
+    rq, rs = R.quantize(x.float())
+    tok = o["perm_token"][:n].long()
+    assert torch.equal(q[:n].double(), rq[tok]) and torch.equal(s[:n].double(), rs[tok, 0])
+    assert (q[n:] == 77).all() and (s[n:] == -1).all()  # rows of no copy, as they were
+
+
 def test_exact_ties_round_to_the_even_code():
     T, d = 2, 64
     cfg = config(T, d, 4, 1, 64)
