@@ -1333,8 +1333,8 @@ moe_status moe_forward_int8(const moe_config *c, const void *x, const float *rou
         return MOE_ERR_CUDA;
     stage.next("moe.expert_ffn");
     // (the one-kernel dispatch also writes the offsets: nothing may be read ahead of it)
-    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, !dispatch_int8_in_one(c->T), ws, L8,
-                 s))
+    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, !dispatch_int8_in_one(c->T, c->K),
+                 ws, L8, s))
         return MOE_ERR_CUDA;
     stage.next("moe.combine");
     return cuda_status(launch_combine(y_perm, inv_perm, topk_w, y_sh, c->T, c->d, c->K,

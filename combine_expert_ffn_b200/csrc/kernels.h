@@ -238,10 +238,13 @@ cudaError_t launch_bias_update(const int32_t *counts, int E, int T, int K, float
                                float *bias, cudaStream_t st);
 // balance.cu: the balance loss and the router's gradient.  Tokens are cut into
 // tiles of balance_tile(T): two tiles per SM for long batches, and at least 32
-// tokens (one per lane group of a block) for short ones.  part and part_n
+// tokens (two or four per lane group of a block) for short ones; up to 1024 tokens
+// make at most BAL_CLUSTER tiles, the blocks of one cluster.  part and part_n
 // ([tiles, 2, E] each) hold the tiles' shares of the sequences that cross them.
+constexpr int BAL_CLUSTER = 8;
 inline int balance_tile(int T) {
-    const int c = (int)(((int64_t)T + 2 * 148 - 1) / (2 * 148));
+    const int tiles = T <= 1024 ? BAL_CLUSTER : 2 * 148;
+    const int c = (int)(((int64_t)T + tiles - 1) / tiles);
     return c < 32 ? 32 : c;
 }
 cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
@@ -272,9 +275,13 @@ cudaError_t launch_quantize_rows_f32(const float *x, int64_t rows, int cols, int
                                      int8_t *q2, float *scale2, cudaStream_t st);
 cudaError_t launch_quantize_joint_bf16(const void *x, int n_mat, int64_t rows, int cols,
                                        int8_t *q, float *scale, cudaStream_t st);
-// The dispatch with int8 rows; one kernel for batches of one dispatch block, which
-// then writes offsets, else the plan of dispatch.cu and the gather behind it.
-inline bool dispatch_int8_in_one(int T) { return T > 0 && T <= DISPATCH_BLOCK; }
+// The dispatch with int8 rows; one kernel for batches of one dispatch block and 4096
+// copies, which then writes offsets, else the plan of dispatch.cu and the gather behind
+// it.  (256 tokens of 2048 over 256 experts, one kernel and three: K = 16 9.0 and 23.9
+// us, K = 32 46 and 46: block 0's counts of the batch grow with the copies.)
+inline bool dispatch_int8_in_one(int T, int K) {
+    return T > 0 && T <= DISPATCH_BLOCK && T * K <= 4096;
+}
 cudaError_t launch_dispatch_int8(const void *x, const int32_t *topk_idx, int T, int d, int E, int G,
                                  int K, int32_t *counts, int32_t *offsets, int32_t *send,
                                  int32_t *send_tok, int32_t *perm_token, int32_t *inv_perm,

@@ -217,7 +217,7 @@ quantize_rows_kernel(const QuantArgs a) {
 // token.  Every block builds the plan for itself -- a bit for each (expert, token), whose
 // counts over all tokens, scanned over the experts, are the offsets, and over the tokens
 // below its own the ranks -- and then writes its token's codes to its K rows; block 0
-// writes what belongs to the batch.  The ids (at most 8192) come from L2 for each block,
+// writes what belongs to the batch.  The ids (at most 4096) come from L2 for each block,
 // which is less than the two launches it saves: 1, 128 and 256 tokens of 7168, K = 8, 256
 // experts take 5.8, 7.0 and 9.3 us, the plan's two kernels and the gather 12.7, 15.5 and 18.8.
 struct SmallDispatch {
@@ -467,7 +467,7 @@ cudaError_t launch_dispatch_int8(const void *x, const int32_t *topk_idx, int T, 
     q.q = x_q; q.scale = x_q_scale;
     q.inv_perm = inv_perm; q.K = K; q.n_perm = (int64_t)T * K;
     q.q_perm = x_perm_q; q.scale_perm = x_scale;
-    if (dispatch_int8_in_one(T)) {
+    if (dispatch_int8_in_one(T, K)) {
         SmallDispatch a{q, topk_idx, T, E, G, counts, offsets, send, send_tok, perm_token, inv_perm,
                         status};
         const size_t smem = sizeof(uint32_t) * ((size_t)E * (DISPATCH_BLOCK / 32) + E + 1 + 2 * G * G);

@@ -91,6 +91,7 @@ def test_dispatch_int8(T, d, E, K):
 
 @pytest.mark.parametrize("T,d,E,G,K,M", [(4, 64, 16, 4, 4, 2), (64, 128, 16, 4, 4, 2),
                                          (256, 192, 256, 8, 8, 4), (256, 64, 1024, 64, 32, 32),
+                                         (128, 64, 1024, 64, 32, 32),
                                          (255, 8256, 40, 5, 6, 2), (257, 320, 12, 1, 4, 1),
                                          (264, 320, 12, 4, 4, 2), (1, 64, 1, 1, 1, 1)])
 @pytest.mark.parametrize("bad", [False, True])

@@ -22,8 +22,8 @@ def cfg_of(T, E, K, router=0, d=64):
     return moe.MoeConfig(T, d, E, 1, K, 1, 64, 0, 0, router, 0)
 
 
-def tile(T):
-    return max(32, -(-T // 296))
+def tile(T):  # tokens of a block
+    return max(32, -(-T // (8 if T <= 1024 else 296)))
 
 
 def inputs(T, E, K, router=0, seed=0):

@@ -63,7 +63,7 @@ def test_balance_loss_arguments(moe):
 def test_balance_tiles_fit_the_workspace(moe):
     """The tiles' shares, 16 E bytes a tile, against the 4 T E bytes of the affinities' region."""
     for T in [*range(1, 2000), 9472, 9473, 262144, 2 ** 26 - 1]:
-        tile = max(32, -(-T // 296))
+        tile = max(32, -(-T // (8 if T <= 1024 else 296)))
         tiles = -(-T // tile)
         assert tiles == 1 or 4 * tiles <= T
 
