@@ -217,8 +217,8 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
     if (!p.early) dependency_wait();
     dependency_release();
     for (int e = threadIdx.x; e < p.E; e += NUM_THREADS) {
-        int lo = p.offsets[e], cnt = 0;
-        const int64_t n = (int64_t)p.offsets[e + 1] - lo;
+        int lo = __ldcg(p.offsets + e), cnt = 0;
+        const int64_t n = (int64_t)__ldcg(p.offsets + e + 1) - lo;
         // a segment that leaves the buffer or has a negative length is treated as
         // empty and reported
         if (lo < 0 || n < 0 || lo + n > p.rows_r) {
@@ -395,7 +395,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             const bool shared = t.e < 0;
             const int n_out = shared ? p.n_out_s : p.n_out_r;
             const float *xs_g = (shared ? p.x_scale_s : p.x_scale_r) + t.t0;
-            for (int j = lane; j < t.n; j += 32) xs[j] = j < t.valid ? xs_g[j] : 0.f;
+            for (int j = lane; j < t.n; j += 32) xs[j] = j < t.valid ? __ldcg(xs_g + j) : 0.f;
             // this lane's channel (whole warps are inside or outside n_out, a multiple of 64)
             const int ch = EPI == EPI_SWIGLU ? t.c0 + rank * 64 + q * 16 + (lane & 15)
                                              : t.c0 + rank * 128 + q * 32 + lane;
