@@ -457,6 +457,13 @@ route_backward_kernel(const RouteGradArgs a) {
 #pragma unroll
             for (int q = 0; q < NV; ++q) v[q] = fabsf(v[q]) < INFINITY ? v[q] : 0.f;
         }
+        // The gates' gradients less the first one's: their mean is taken off them below, so
+        // it makes no difference but that equal ones (or a single one) cancel exactly.
+        if (gate) {
+            const float dw0 = __shfl_sync(0xFFFFFFFFu, dw[0], lane - glane);
+#pragma unroll
+            for (int h = 0; h < SLOTS; ++h) dw[h] -= dw0;
+        }
         // the four sums of a token side by side: S, pull . s, Z, dw . s_chosen
         float sum = 0.f, dot = 0.f, z = 0.f, zdw = 0.f, down = 1.0f;
         auto sums = [&] {

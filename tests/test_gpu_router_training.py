@@ -288,6 +288,24 @@ def test_route_backward_bad_and_repeated_ids():
     assert ((out.double() - ref).abs() <= 2 * route_bound(s, twice, dw, zero, 0) + 1e-30).all()
 
 
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("T,E,K", [(70, 64, 1), (33, 256, 1), (50, 30, 1), (40, 1024, 1), (64, 64, 6),
+                                   (40, 24, 12), (21, 254, 31)])
+def test_route_backward_of_equal_gate_gradients_is_the_balance_losss(T, E, K, router):
+    """Gates sum to 1: a gradient that all gates of a token share (any, with a single gate) moves
+    nothing, and must not leave its rounding behind beside a much smaller balance gradient."""
+    cfg, alpha = cfg_of(T, E, K, router), 1e-6
+    s, idx, g = inputs(T, E, K, router)
+    o = [0, T // 3, T]
+    n = R.counts(idx, o, E).int()
+    dl = torch.ones(2, device=DEV)
+    dw = 1e3 * torch.randn(T, 1, device=DEV, generator=g).expand(T, K).contiguous()
+    both, alone = torch.empty(T, E, device=DEV), torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(cfg, s, idx, dw, offsets(o), n, dl, alpha, both)
+    moe.moe_route_backward(cfg, s, idx, None, offsets(o), n, dl, alpha, alone)
+    assert torch.equal(both, alone)
+
+
 @pytest.mark.parametrize("T,E,K", [(40, 24, 12), (33, 256, 17), (20, 30, 9)])
 def test_route_backward_repeated_ids_in_long_choices(T, E, K):
     """Two gates of one expert where a lane holds several of a token's gates."""
