@@ -403,6 +403,7 @@ route_backward_kernel(const RouteGradArgs a) {
             if (in && (i[h] < 0 || i[h] >= a.E)) {
                 record_status(a.status, MOE_ERR_DEVICE_FAULT);
                 i[h] = -1;
+                d[h] = 0.f;
             }
         }
     };

@@ -306,6 +306,21 @@ def test_route_backward_of_equal_gate_gradients_is_the_balance_losss(T, E, K, ro
     assert torch.equal(both, alone)
 
 
+@pytest.mark.parametrize("T,E,K", [(40, 16, 4), (33, 256, 17), (20, 30, 9)])
+@pytest.mark.parametrize("slot", [0, 2])
+def test_route_backward_does_not_read_the_gradient_of_a_skipped_gate(T, E, K, slot):
+    cfg = cfg_of(T, E, K)
+    s, idx, g = inputs(T, E, K)
+    idx[5, slot], idx[T - 1, slot] = E, -1
+    dw = torch.randn(T, K, device=DEV, generator=g)
+    dw[5, slot] = dw[T - 1, slot] = 0.0
+    want, out = torch.empty(T, E, device=DEV), torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(cfg, s, idx, dw, None, None, None, 0.0, want)
+    dw[5, slot], dw[T - 1, slot] = float("nan"), 1e30
+    moe.moe_route_backward(cfg, s, idx, dw, None, None, None, 0.0, out)
+    assert torch.equal(want, out) and want.isfinite().all()
+
+
 @pytest.mark.parametrize("T,E,K", [(40, 24, 12), (33, 256, 17), (20, 30, 9)])
 def test_route_backward_repeated_ids_in_long_choices(T, E, K):
     """Two gates of one expert where a lane holds several of a token's gates."""
