@@ -22,7 +22,10 @@
 // products.  An expert's tokens are cut into equal tiles of at most 256, so at
 // most 31 padding columns are computed per expert: with the tokens on M, in tiles
 // of 128, a quarter of the MMA work of a 256-token expert was padding, and a
-// decode step's (a few tokens per expert) nearly all of it.
+// decode step's (a few tokens per expert) nearly all of it.  An expert of little more
+// than 256 tokens would have two small tiles that each load all its weights: the WIDE
+// kernel makes one of them, over both accumulators; a k block then takes two stages, the
+// second one with tokens only, and both products read the first one's weights.
 //   GEMM1  a tile's 256 weight rows are 128 channels' gate and up rows, 16 and 16
 //          in turn (one 16 KB TMA box over both tensors: boxes of 16 rows each made
 //          this GEMM 1.5 times slower at a decode step, 1745 against 1149 us): one
@@ -41,10 +44,11 @@
 //   128 tokens   1.69 ms for 11.2 GB, 6.6 TB/s: HBM bounds it
 //   1 token      78 us for 0.40 GB, 5.1 TB/s: the first loads of each GEMM and the last,
 //                partly filled round of tiles (252 of GEMM2 over 74 pairs)
-//   8192 tokens  4.1 ms, 1.6 POP/s: the power limit.  Back to back passes run at 1.05 to
-//                1.1 GHz; the first ones, at up to 1.9 GHz, take 3.3 ms.  The products
-//                alone (no loads, no epilogue) would take 2.3 ms at the same power, the
-//                token loads cost 0.7, the weight loads 1.4, epilogue and h 0.6 ms
+//   8192 tokens  3.85 to 4.1 ms (by the GPU), 1.6 POP/s: the power limit.  Back to back
+//                passes run at 1.05 to 1.1 GHz, the first ones at up to 1.9 GHz.  Of 4.1 ms
+//                before the wide tiles (which saved 0.23) the products alone would take 2.3
+//                at the same power, the token loads cost 0.7, the weight loads 1.4,
+//                epilogue and h 0.6
 #include <cstring>
 
 #include "kernels.h"
@@ -54,7 +58,8 @@ namespace gemm_i8 {
 
 constexpr int BK = 128;            // codes (bytes) per k block
 constexpr int M_CTA = 128;         // weight rows of a CTA; the pair has twice as many
-constexpr int N_MAX = 256;         // tokens of a tile
+constexpr int N_MAX = 256;         // tokens of an accumulator
+constexpr int WIDE_MAX = 2 * N_MAX;  // ... and of a tile that takes both
 constexpr int N_STEP = 32;
 constexpr int STAGES = 6;
 constexpr int A_BYTES = M_CTA * BK;
@@ -97,22 +102,29 @@ struct Tile {
     int e;           // expert, or -1: the shared experts
     int c0;          // first channel of the pair
     int t0, valid;   // first token row, rows to store
-    int n;           // MMA columns, a multiple of N_STEP
+    int n, n1;       // MMA columns of the first and the second (or 0) accumulator
     int kblocks;
 };
 
-// Token tiles of an expert: the fewest of at most N_MAX, equal up to N_STEP.
-__device__ __forceinline__ int token_tiles(int cnt) { return (cnt + N_MAX - 1) / N_MAX; }
+// Token tiles of an expert: the fewest of at most N_MAX, equal up to N_STEP.  WIDE: a
+// single one up to WIDE_MAX.
+template <bool WIDE>
+__device__ __forceinline__ int token_tiles(int cnt) {
+    return WIDE && cnt <= WIDE_MAX ? cnt > 0 : (cnt + N_MAX - 1) / N_MAX;
+}
+template <bool WIDE>
 __device__ __forceinline__ void token_range(int cnt, int tiles, int i, Tile &t) {
     const int units = (cnt + N_STEP - 1) / N_STEP;
     const int each = units / tiles, more = units - each * tiles;
     const int u0 = i * each + min(i, more);
     t.t0 = u0 * N_STEP;
-    t.n = (each + (i < more)) * N_STEP;
-    t.valid = min(t.n, cnt - t.t0);
+    const int mine = each + (i < more);
+    t.n1 = WIDE && mine * N_STEP > N_MAX ? mine / 2 * N_STEP : 0;
+    t.n = mine * N_STEP - t.n1;
+    t.valid = min(mine * N_STEP, cnt - t.t0);
 }
 
-template <int EPI>
+template <int EPI, bool WIDE>
 __device__ __forceinline__ Tile decode_tile(int idx, const int *tile_base, const int *seg,
                                             const int *segc, const Params &p, int ntr, int nc_s) {
     Tile t;
@@ -122,10 +134,10 @@ __device__ __forceinline__ Tile decode_tile(int idx, const int *tile_base, const
             const int mid = (lo + hi) >> 1;
             if (tile_base[mid] <= idx) lo = mid; else hi = mid;
         }
-        const int cnt = segc[lo], nt = token_tiles(cnt);
+        const int cnt = segc[lo], nt = token_tiles<WIDE>(cnt);
         const int local = idx - tile_base[lo];
         const int c = local / nt;  // token tiles of the same weights side by side
-        token_range(cnt, nt, local - c * nt, t);
+        token_range<WIDE>(cnt, nt, local - c * nt, t);
         t.t0 += seg[lo];
         t.c0 = c * channels<EPI>();
         t.e = lo;
@@ -133,7 +145,7 @@ __device__ __forceinline__ Tile decode_tile(int idx, const int *tile_base, const
     } else {
         const int local = idx - ntr;
         const int i = local / nc_s;
-        token_range(p.T, token_tiles(p.T), i, t);
+        token_range<WIDE>(p.T, token_tiles<WIDE>(p.T), i, t);
         t.c0 = (local - i * nc_s) * channels<EPI>();
         t.e = -1;
         t.kblocks = p.n_seg_s * ((p.k_s + BK - 1) / BK);
@@ -168,7 +180,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-template <int EPI>
+template <int EPI, bool WIDE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -238,7 +250,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int per = (p.E + 31) / 32;
         const int e0 = min(p.E, lane * per), e1 = min(p.E, e0 + per);
         int mine = 0;
-        for (int e = e0; e < e1; ++e) mine += token_tiles(segc[e]) * nc_r;
+        for (int e = e0; e < e1; ++e) mine += token_tiles<WIDE>(segc[e]) * nc_r;
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -248,7 +260,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         int at = incl - mine;
         for (int e = e0; e < e1; ++e) {
             tile_base[e] = at;
-            at += token_tiles(segc[e]) * nc_r;
+            at += token_tiles<WIDE>(segc[e]) * nc_r;
         }
         if (lane == 31) tile_base[p.E] = incl;
     }
@@ -259,7 +271,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     const int ntr = tile_base[p.E];
     const int nc_s = p.T > 0 ? (p.n_out_s + channels<EPI>() - 1) / channels<EPI>() : 0;
-    const int total = ntr + (p.T > 0 ? token_tiles(p.T) * nc_s : 0);
+    const int total = ntr + (p.T > 0 ? token_tiles<WIDE>(p.T) * nc_s : 0);
     const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
 
     if (warp == 0) {
@@ -270,17 +282,15 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         bool ok = true;
         const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);  // the leader's
         for (int idx = pair_id; idx < total && ok; idx += n_pairs) {
-            const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nc_s);
+            const Tile t = decode_tile<EPI, WIDE>(idx, tile_base, seg, segc, p, ntr, nc_s);
             const bool shared = t.e < 0;
             const CUtensorMap *w = shared ? &maps.w_s : &maps.w_r;
             const CUtensorMap *x = shared ? maps.x_s : maps.x_r;
             const int k_len = shared ? p.k_s : p.k_r;
             const int ch = t.c0 + rank * (channels<EPI>() / 2);
-            const int half = t.n / 2, tok = t.t0 + rank * half;
-            // the half as boxes of 64, 32 and 16 rows
-            const int r32 = half & ~63, r16 = half & ~31;
-            const uint32_t tx = 2 * (A_BYTES + (uint32_t)half * BK);
+            const int runs = WIDE && t.n1 ? 2 : 1;  // stages of a k block
             int mat = shared ? 0 : t.e, k = 0, x_col = 0;
+            const uint32_t tx = 2 * A_BYTES + (uint32_t)t.n * BK;
             auto load_weights = [&](int s) {
                 const uint32_t fb = full0 + 8 * s, a_dst = smem0 + s * STAGE_BYTES;
                 if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), tx);
@@ -300,32 +310,50 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             };
             int ahead = 0;  // k blocks of the first tile whose weights are on their way
             if (p.early && idx == pair_id) {
-                for (; ahead < min(STAGES, t.kblocks); ++ahead) {
-                    if (elect_one()) load_weights(ahead);
+                for (; ahead < min(STAGES / runs, t.kblocks); ++ahead) {
+                    if (elect_one()) load_weights(ahead * runs);
                     __syncwarp();
                     advance();
                 }
                 mat = shared ? 0 : t.e, k = 0, x_col = 0;
                 dependency_wait();
             }
+            // this CTA's half of an accumulator's tokens as boxes of 64, 32 and 16 rows
+            auto load_tokens = [&](int first, int half) {
+                const uint32_t fb = full0 + 8 * stage;
+                const uint32_t b_dst = smem0 + stage * STAGE_BYTES + A_BYTES;
+                const int r32 = half & ~63, r16 = half & ~31, tok = first + rank * half;
+                if (half & 16) tma_load_2d_pair(b_dst + r16 * BK, x + 2, fb, x_col + k, tok + r16);
+                if (half & 32) tma_load_2d_pair(b_dst + r32 * BK, x + 1, fb, x_col + k, tok + r32);
+                if (half >= 64) tma_load_2d_pair(b_dst, x, fb, x_col + k, tok);
+                if (half == 128) tma_load_2d_pair(b_dst + 64 * BK, x, fb, x_col + k, tok + 64);
+            };
             for (int kb = 0; kb < t.kblocks; ++kb) {
                 if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p)) {
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t fb = full0 + 8 * stage;
-                    const uint32_t b_dst = smem0 + stage * STAGE_BYTES + A_BYTES;
                     if (kb >= ahead) load_weights(stage);
-                    if (half & 16) tma_load_2d_pair(b_dst + r16 * BK, x + 2, fb, x_col + k, tok + r16);
-                    if (half & 32) tma_load_2d_pair(b_dst + r32 * BK, x + 1, fb, x_col + k, tok + r32);
-                    if (half >= 64) tma_load_2d_pair(b_dst, x, fb, x_col + k, tok);
-                    if (half == 128) tma_load_2d_pair(b_dst + 64 * BK, x, fb, x_col + k, tok + 64);
+                    load_tokens(t.t0, t.n / 2);
                 }
                 __syncwarp();
-                advance();
                 ++n_issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (WIDE && t.n1) {
+                    if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), t.n1 * BK);
+                        load_tokens(t.t0 + t.n, t.n1 / 2);
+                    }
+                    __syncwarp();
+                    ++n_issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                advance();
             }
         }
         if (p.early && pair_id >= total) dependency_wait();
@@ -343,38 +371,65 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         // ------------------------------------------------------ MMA issuer (leader)
         // The whole warp walks the tiles and waits; one elected lane issues.
         if (leader) {
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
+            int stage = 0;
+            uint32_t phase = 0, use = 0;  // accumulators so far, in turn
             bool ok = true;
             for (int idx = pair_id; idx < total && ok; idx += n_pairs) {
-                const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nc_s);
+                const Tile t = decode_tile<EPI, WIDE>(idx, tile_base, seg, segc, p, ntr, nc_s);
                 const uint32_t idesc = idesc_s8_s32(2 * M_CTA, t.n);
-                if (!warp_wait(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * N_MAX;
+                const uint32_t idesc1 = idesc_s8_s32(2 * M_CTA, t.n1);
+                const uint32_t d_tmem = tmem_base + (use & 1u) * N_MAX;
+                const uint32_t d1_tmem = tmem_base + (~use & 1u) * N_MAX;
+                if (!warp_wait(smem_u32(&tempty_bar[use & 1u]), (use >> 1 & 1u) ^ 1u, abort_flag, p))
+                    break;
                 for (int kb = 0; kb < t.kblocks; ++kb) {
                     if (!warp_wait(smem_u32(&full_bar[stage]), phase, abort_flag, p)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
+                    const int first = stage;
+                    const uint32_t a_addr = smem0 + stage * STAGE_BYTES;
+                    const uint64_t a_desc = smem_desc_sw128(a_addr);
                     if (elect_one()) {
-                        const uint32_t a_addr = smem0 + stage * STAGE_BYTES;
-                        const uint64_t a_desc = smem_desc_sw128(a_addr);
                         const uint64_t b_desc = smem_desc_sw128(a_addr + A_BYTES);
 #pragma unroll
                         for (int ks = 0; ks < BK / 32; ++ks)
                             tc_mma_s8_pair(d_tmem, a_desc + 2 * ks, b_desc + 2 * ks, idesc,
                                            (kb | ks) != 0 ? 1u : 0u);
-                        tc_commit_pair_both(smem_u32(&empty_bar[stage]));
+                        if (!WIDE || !t.n1) tc_commit_pair_both(smem_u32(&empty_bar[stage]));
                     }
                     __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (WIDE && t.n1) {  // the same weights with the second accumulator's tokens
+                        if ((kb == 0 && !warp_wait(smem_u32(&tempty_bar[~use & 1u]),
+                                                   ((use + 1) >> 1 & 1u) ^ 1u, abort_flag, p)) ||
+                            !warp_wait(smem_u32(&full_bar[stage]), phase, abort_flag, p)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t b_desc =
+                                smem_desc_sw128(smem0 + stage * STAGE_BYTES + A_BYTES);
+#pragma unroll
+                            for (int ks = 0; ks < BK / 32; ++ks)
+                                tc_mma_s8_pair(d1_tmem, a_desc + 2 * ks, b_desc + 2 * ks, idesc1,
+                                               (kb | ks) != 0 ? 1u : 0u);
+                            tc_commit_pair_both(smem_u32(&empty_bar[first]));
+                            tc_commit_pair_both(smem_u32(&empty_bar[stage]));
+                        }
+                        __syncwarp();
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    }
                 }
                 if (!ok) break;
-                if (elect_one()) tc_commit_pair_both(smem_u32(&tfull_bar[acc]));
+                if (elect_one()) {
+                    tc_commit_pair_both(smem_u32(&tfull_bar[use & 1u]));
+                    if (WIDE && t.n1) tc_commit_pair_both(smem_u32(&tfull_bar[(use + 1) & 1u]));
+                }
                 __syncwarp();
-                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                use += WIDE && t.n1 ? 2 : 1;
             }
             // wind down: every MMA issued has completed
             if (elect_one()) tc_commit_pair(smem_u32(&done_bar));
@@ -388,10 +443,20 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int part = (warp - 2) >> 2;
         float *xs = x_scale[warp - 2];
         if (p.early) dependency_wait();
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int idx = pair_id; idx < total; idx += n_pairs) {
-            const Tile t = decode_tile<EPI>(idx, tile_base, seg, segc, p, ntr, nc_s);
+        uint32_t use = 0;
+        int second = 0;  // the tokens that a tile's second accumulator has yet
+        for (int idx = pair_id; idx < total; idx += WIDE && second ? 0 : n_pairs, ++use) {
+            Tile t = decode_tile<EPI, WIDE>(idx, tile_base, seg, segc, p, ntr, nc_s);
+            const uint32_t acc = use & 1u;
+            if (WIDE && second) {
+                t.t0 += t.n;
+                t.valid -= t.n;
+                t.n = t.n1;
+                second = 0;
+            } else if (WIDE) {
+                second = t.n1;
+                t.valid = min(t.valid, t.n);
+            }
             const bool shared = t.e < 0;
             const int n_out = shared ? p.n_out_s : p.n_out_r;
             const float *xs_g = (shared ? p.x_scale_s : p.x_scale_r) + t.t0;
@@ -408,7 +473,7 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
                                                                  ch];
             }
             __syncwarp();
-            if (!mbar_wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, p.status,
+            if (!mbar_wait_bounded(smem_u32(&tfull_bar[acc]), use >> 1 & 1u, abort_flag, p.status,
                                    p.timeout_ns))
                 break;
             tc_fence_after();
@@ -461,7 +526,6 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
     }
 
@@ -485,14 +549,25 @@ int sm_count() {
 }
 
 template <int EPI>
-cudaError_t launch(const Maps &maps, const Params &p, cudaStream_t st) {
-    auto kern = grouped_int8_kernel<EPI>;
+cudaError_t launch(const Maps &maps, const Params &p, const FfnInt8Args &a, cudaStream_t st) {
+    const int sms = sm_count() / 2 * 2;
+    // Wide tiles pay where most experts have 257 to 512 tokens or little less, whose
+    // weights would be loaded twice and in smaller tiles, where the reduction is long (an
+    // epilogue no longer runs beside the next tile's products) and where each pair gets
+    // many tiles (they are coarser).  us without and with:
+    //   256 experts of 7168 x 2048, K = 8: 8192 tokens 4370 4140, 9216 5040 4430, 12288
+    //   5750 5140; 4096 2650 2690 and 16384 (512 an expert and more) 6530 6910
+    //   (64 of 2048 x 1408, 4096 tokens of 6: 380 434; 32 of 7168 x 2048, 1024 of 8: 445 500)
+    const int64_t rows = (int64_t)a.T * a.K, blocks = (p.n_out_r + channels<EPI>() - 1) / channels<EPI>();
+    const bool wide = rows >= 192ll * a.E && rows <= 448ll * a.E && p.k_r >= 32 * BK &&
+                      a.E * blocks >= 32ll * (sms / 2);
+    auto kern = wide ? grouped_int8_kernel<EPI, true> : grouped_int8_kernel<EPI, false>;
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_DYN);
     if (err != cudaSuccess) return err;
     // one wave of pairs, one CTA per SM (pairs that do not fit at once would take
     // their share of the tiles later)
-    return launch_dependent(kern, sm_count() / 2 * 2, NUM_THREADS, SMEM_DYN, 2, st, maps, p);
+    return launch_dependent(kern, sms, NUM_THREADS, SMEM_DYN, 2, st, maps, p);
 }
 
 // Token codes [rows, cols] in boxes of 64, 32 and 16 rows.
@@ -548,7 +623,7 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
     p.status = a.status;
     p.timeout_ns = a.timeout_ns;
     p.early = a.after_quantize;
-    cudaError_t err = launch<EPI_SWIGLU>(m, p, st);
+    cudaError_t err = launch<EPI_SWIGLU>(m, p, a, st);
     if (err != cudaSuccess) return err;
 
     err = launch_quantize_rows_f32(a.h, (int64_t)rows, a.d_ff, a.h_q, a.h_scale, a.h_shared,
@@ -573,7 +648,7 @@ cudaError_t launch_expert_ffn_int8(const FfnInt8Args &a, cudaStream_t st) {
     p.out_r = a.y_perm;
     p.out_s = a.y_shared;
     p.early = 1;  // (behind the quantization of h)
-    return launch<EPI_STORE>(m, p, st);
+    return launch<EPI_STORE>(m, p, a, st);
 }
 
 }  // namespace moe

@@ -241,6 +241,35 @@ def test_gate_and_up_in_either_order_of_addresses():
     check_ffn(cfg, xq, xs, offsets, w, x, y, sh)
 
 
+def test_tiles_of_more_than_256_tokens_give_the_same_bits():
+    """152 experts of 4096 x 4160 with 0 to 700 tokens take tiles of up to 512 tokens in both
+    products (the averages and lengths that choose them); 8 or 16 experts of them at a time do not.
+    Integer sums and the same roundings: equal bits, the shared experts' among them."""
+    E, K, T, d, ff = 152, 8, 4864, 4096, 4160
+    cfg, g = config(T, d, E, K, ff, 1, 128), gen(21)
+    counts = [0, 1, 255, 256, 257, 288, 289, 320, 384, 415, 416, 480, 511, 512, 513, 700]
+    rest = T * K - sum(counts) - 40  # (40 rows in no segment)
+    counts += [rest // (E - 16)] * (E - 17)
+    counts += [T * K - 40 - sum(counts)]
+    offsets = torch.tensor([0] + counts).cumsum(0).int().to(DEV)
+    xq = torch.randint(-127, 128, (T * K, d), dtype=torch.int8, device=DEV, generator=g)
+    xs = torch.rand(T * K, device=DEV, generator=g) / 74 + 1e-3
+    x = torch.randn(T, d, device=DEV, generator=g).bfloat16()
+    w = random_weights(cfg, g)
+    y, sh, ws = run_ffn(cfg, xq, xs, offsets, w, x)
+    assert not y[:-40].isnan().any() and y[-40:].isnan().all()
+    for e, n in ((0, 8), (8, 8), (136, 16)):
+        lo, hi = int(offsets[e]), int(offsets[e + n])
+        part = config(-(-(hi - lo) // K), d, n, K, ff, 1, 128)
+        rows = part.T * K
+        pad = lambda t: torch.cat([t[lo:hi], t[:rows - (hi - lo)]])
+        some = {k: v if k.startswith("ws_") else v[e:e + n].clone() for k, v in w.items()}
+        seg = (offsets[e:e + n + 1] - lo).contiguous()
+        y2, sh2, _ = run_ffn(part, pad(xq), pad(xs), seg, some, x[:part.T].contiguous())
+        assert torch.equal(y[lo:hi], y2[:hi - lo]) and torch.equal(sh[:part.T], sh2)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+
+
 def test_rows_behind_the_2_to_the_31st_byte():
     """Dispatch, experts and the combine's gradient at 300,032 rows of 7168: codes pass 2^31 bytes,
     bf16 rows 2^32.  The last rows against their definition, the dispatch in full."""
