@@ -538,6 +538,8 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
         tc_fence_after();
         tmem_dealloc_pair<TMEM_COLS>(tmem_base);
     }
+    __syncwarp();
+    cluster_sync_all();  // neither CTA is gone while the other still frees the pair's TMEM
 }
 
 namespace {
