@@ -42,9 +42,9 @@
 //
 // Measured with d = 7168, 256 experts of d_ff 2048, K = 8 and one shared expert:
 //   128 tokens   1.69 ms for 11.2 GB, 6.6 TB/s: HBM bounds it
-//   1 token      78 us for 0.40 GB, 5.1 TB/s: the first loads of each GEMM and the last,
+//   1 token      79 us for 0.40 GB, 5.0 TB/s: the first loads of each GEMM and the last,
 //                partly filled round of tiles (252 of GEMM2 over 74 pairs)
-//   8192 tokens  3.85 to 4.1 ms (by the GPU), 1.6 POP/s: the power limit.  Back to back
+//   8192 tokens  3.8 to 4.2 ms (by the GPU), 1.6 POP/s: the power limit.  Back to back
 //                passes run at 1.05 to 1.1 GHz, the first ones at up to 1.9 GHz.  Of 4.1 ms
 //                before the wide tiles (which saved 0.23) the products alone would take 2.3
 //                at the same power, the token loads cost 0.7, the weight loads 1.4,
@@ -473,9 +473,8 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
                                                                  ch];
             }
             __syncwarp();
-            if (!mbar_wait_bounded(smem_u32(&tfull_bar[acc]), use >> 1 & 1u, abort_flag, p.status,
-                                   p.timeout_ns))
-                break;
+            // (the TMEM loads want the warp together)
+            if (!warp_wait(smem_u32(&tfull_bar[acc]), use >> 1 & 1u, abort_flag, p)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * N_MAX;
             // which of two neighbouring tokens this lane stores
