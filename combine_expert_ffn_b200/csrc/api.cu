@@ -337,7 +337,7 @@ moe_status moe_balance_loss(const moe_config *c, const float *scores, const int3
     StageRange range("moe.balance_loss");
     // the tiles' shares ([tiles, 2, E] floats and as many counts) fit the region of
     // the affinities: where there are two tiles or more, T >= 4 * tiles
-    const int tile = balance_tile(c->T);
+    const int tile = balance_tile(c->T, n_seq);
     const int tiles = (int)(((int64_t)c->T + tile - 1) / tile);
     float *part = at<float>(ws, L.scores);
     int32_t *part_n = reinterpret_cast<int32_t *>(part + (size_t)tiles * 2 * c->E);

@@ -598,7 +598,7 @@ cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
                                 int K, int32_t *counts, float *prob, float *loss, float *part,
                                 int32_t *part_n, int32_t *status, cudaStream_t st) {
     if (n_seq == 0) return cudaSuccess;
-    BalanceArgs a{scores, topk_idx, offsets, n_seq, T, E, K, balance_tile(T), alpha,
+    BalanceArgs a{scores, topk_idx, offsets, n_seq, T, E, K, balance_tile(T, n_seq), alpha,
                   counts, prob, loss, part, part_n, status};
     const int tiles = T > 0 ? (T + a.tile - 1) / a.tile : 1;
     const size_t smem = sizeof(float) * (size_t)E * (BAL_WARPS + 1);

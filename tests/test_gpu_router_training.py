@@ -379,6 +379,25 @@ def test_many_short_sequences():
     assert ((loss.double() - ref).abs() <= 64 * U * ref).all()
 
 
+@pytest.mark.parametrize("T,E,K", [(1000, 40, 6), (300, 256, 8), (70000, 30, 2)])
+def test_a_long_sequence_among_short_ones(T, E, K):
+    """Short tiles for the many short ones, and so many shares of the long one.  Its p is a sum of
+    at most tile terms a lane, of a block's, and of the tiles in as many chains as the join's 1024
+    threads allow; each addition of fp32 is off by U of a sum of positive terms."""
+    cfg, alpha = cfg_of(T, E, K), 0.5
+    s, idx, _ = inputs(T, E, K)
+    o = [*range(0, T // 8), *range(T // 8, T // 4, 5), T // 4, T - T // 8, *range(T - T // 8 + 3, T, 7), T]
+    n, p, loss, ws = balance(cfg, s, idx, offsets(o), alpha)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    ref_n = R.counts(idx, o, E)
+    assert torch.equal(n.long(), ref_n)
+    ref_p, ref_loss = R.balance_loss(s.double(), ref_n, o, alpha, K)
+    short = max(8, T // (len(o) - 1), T // 2048)
+    bound = (40 + short / 8 + 2 + 17 + T / short / (1024 // (-(-E // 32) * 32)) + 41) * U
+    assert ((p.double() - ref_p).abs() <= bound * ref_p).all()
+    assert ((loss.double() - ref_loss).abs() <= (bound + 4 * U) * ref_loss).all()
+
+
 # ------------------------------------------------------------------ combine gradient
 COMBINE = [(1, 64, 1), (1, 7168, 8), (3, 320, 5), (40, 128, 32), (300, 2048, 6), (700, 576, 8),
            (2500, 64, 1), (9, 8256, 3)]

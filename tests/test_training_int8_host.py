@@ -68,6 +68,16 @@ def test_balance_tiles_fit_the_workspace(moe):
         assert tiles == 1 or 4 * tiles <= T
 
 
+def test_balance_tiles_of_short_sequences_fit_the_workspace(moe):
+    """The same for tiles of an average sequence, 8 tokens or more."""
+    for T in [*range(1, 400), 1024, 1025, 262144]:
+        for n_seq in {1, 2, T // 40 + 1, T // 9 + 1, T, 2 * T, 2 ** 20}:
+            tile, average = max(32, -(-T // (8 if T <= 1024 else 296))), max(8, T // n_seq, T // 2048)
+            tile = average if 2 * average <= tile else tile
+            tiles = -(-T // tile)
+            assert tiles == 1 or 4 * tiles <= T
+
+
 def test_route_backward_arguments(moe):
     c = cfg(moe)
     lib = moe._lib.moe_route_backward
