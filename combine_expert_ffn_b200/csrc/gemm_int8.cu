@@ -357,14 +357,16 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
             }
         }
         if (p.early && pair_id >= total) dependency_wait();
-        // wind down (leader): every load of both CTAs has landed
-        if (leader) {
-            for (int s = 0; s < STAGES; ++s) {
-                if (n_issued > (uint32_t)s) {
-                    const uint32_t uses = (n_issued - 1 - s) / STAGES + 1;
-                    drain_wait(smem_u32(&full_bar[s]), (uses - 1) & 1u, p.timeout_ns, p.status);
-                }
-            }
+        // Wind down: every load of both CTAs has landed (the leader's barriers count both),
+        // and every stage's last release has arrived in this CTA.  The commits behind those
+        // releases are arrivals from the leader's tensor core, in both CTAs and asynchronous:
+        // no barrier of the threads orders them, and one that came late would hit the shared
+        // memory of a CTA that is gone or of the block in its place.  Where a wait ran out,
+        // no commit of the last two seconds is under way, and stages may never be released.
+        for (int s = 0; s < min(STAGES, (int)n_issued); ++s) {
+            const uint32_t last = ((n_issued - 1 - s) / STAGES) & 1u;  // parity of its last use
+            if (leader) drain_wait(smem_u32(&full_bar[s]), last, p.timeout_ns, p.status);
+            ok = ok && warp_wait(smem_u32(&empty_bar[s]), last, abort_flag, p);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -530,8 +532,8 @@ grouped_int8_kernel(const __grid_constant__ Maps maps, const Params p) {
 
     tc_fence_before();
     __syncthreads();
-    // the leader's MMAs into this CTA's TMEM and every load into this CTA's
-    // shared memory are done before either CTA frees TMEM or exits
+    // the leader's MMAs into this CTA's TMEM, every load into this CTA's shared memory
+    // and every arrival on its barriers are done before either CTA frees TMEM or exits
     cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();

@@ -464,3 +464,20 @@ def test_python_entry_points_refuse_wrong_tensors():
         moe.Int8Weights(w_gate=w["w_gate"].transpose(1, 2))
     with pytest.raises(TypeError):
         moe.Int8Weights(gate=w["w_gate"])
+
+
+# ------------------------------------------------------------------ short kernels one behind the other
+@pytest.mark.parametrize("d,d_ff", [(64, 64), (128, 64), (704, 320), (768, 768), (832, 1472)])
+def test_short_pair_kernels_behind_one_another(d, d_ff):
+    """Tiles of 1 to 13 k blocks on a ring of six stages, from one tile up to several a pair, three
+    hundred calls without a pause: a block's last stages are still being released when the next
+    kernel's blocks want its place."""
+    for T, E, K in ((1, 1, 1), (3, 5, 2), (64, 24, 4)):
+        cfg, xq, xs, offsets, w, x = ffn_inputs((T, d, E, K, d_ff, 1, 64, 0.0))
+        y, sh, ws = run_ffn(cfg, xq, xs, offsets, w, x)
+        weights, y2, sh2 = moe.Int8Weights(**w), torch.empty_like(y), torch.empty_like(sh)
+        for _ in range(300):
+            moe.moe_expert_ffn_int8(cfg, xq, xs, offsets, weights, y2, x, sh2, ws)
+        assert torch.equal(y, y2) and torch.equal(sh, sh2)
+        assert moe.moe_read_device_status(ws) == moe.MOE_OK
+        check_ffn(cfg, xq, xs, offsets, w, x, y, sh)
