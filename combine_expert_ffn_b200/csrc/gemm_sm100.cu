@@ -1273,7 +1273,8 @@ grouped_ffn_cta2_kernel(const __grid_constant__ Maps maps, const Params p) {
             int stage = 0;
             uint32_t phase = 0;
             uint32_t n_issued = 0;
-            for (int idx = pair_id; idx < total; idx += n_pairs) {
+            bool ok = true;
+            for (int idx = pair_id; idx < total && ok; idx += n_pairs) {
                 const C2Tile t = decode_c2<EPI>(idx, tile_base, seg, segc, p, ntr, nt_s);
                 const int kb_total = t.e >= 0 ? p.k_r / BK : p.k_s / BK;
                 // first 128-byte row of this CTA's half of the (n, kb = 0) weight tile
@@ -1281,7 +1282,6 @@ grouped_ffn_cta2_kernel(const __grid_constant__ Maps maps, const Params p) {
                     (t.e >= 0 ? p.bpk_row_r + ((int64_t)t.e * p.bp_nt_r + t.n0 / BN_OUT) * kb_total * 256
                               : p.bpk_row_s + (int64_t)(t.n0 / BN_OUT) * kb_total * 256) +
                     rank * BM;
-                bool ok = true;
                 for (int kb = 0; kb < t.kblocks; ++kb) {
                     if (!mbar_wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag,
                                            p.status, p.timeout_ns)) {
@@ -1298,16 +1298,16 @@ grouped_ffn_cta2_kernel(const __grid_constant__ Maps maps, const Params p) {
                     ++n_issued;
                     if (++stage == C2_STAGES) { stage = 0; phase ^= 1u; }
                 }
-                if (!ok) break;
             }
-            // wind down (leader): every load of both CTAs has landed
-            if (leader) {
-                for (int s = 0; s < C2_STAGES; ++s) {
-                    if (n_issued > (uint32_t)s) {
-                        const uint32_t uses = (n_issued - 1 - s) / C2_STAGES + 1;
-                        drain_wait(smem_u32(&full_bar[s]), (uses - 1) & 1u, p.timeout_ns, p.status);
-                    }
-                }
+            // wind down: every load of both CTAs has landed (leader), and every stage's last
+            // release, an arrival from the leader's tensor core that the barriers of the
+            // threads do not order, has arrived in this CTA (unless a wait ran out: then no
+            // commit of the last two seconds is under way)
+            for (int s = 0; s < min(C2_STAGES, (int)n_issued); ++s) {
+                const uint32_t last = ((n_issued - 1 - s) / C2_STAGES) & 1u;
+                if (leader) drain_wait(smem_u32(&full_bar[s]), last, p.timeout_ns, p.status);
+                ok = ok && mbar_wait_bounded(smem_u32(&empty_bar[s]), last, abort_flag, p.status,
+                                             p.timeout_ns);
             }
         }
         __syncwarp();
@@ -1441,13 +1441,15 @@ grouped_ffn_cta2_kernel(const __grid_constant__ Maps maps, const Params p) {
     // ---------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
-    // the leader's MMAs into this CTA's TMEM and every load into this CTA's
-    // shared memory are done before either CTA frees TMEM or exits
+    // the leader's MMAs into this CTA's TMEM, every load into this CTA's shared memory
+    // and every arrival on its barriers are done before either CTA frees TMEM or exits
     cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair<TMEM_COLS>(tmem_base);
     }
+    __syncwarp();
+    cluster_sync_all();  // neither CTA is gone while the other still frees the pair's TMEM
 }
 
 // Bounded-wait self-test: one thread waits on a barrier that never completes.
