@@ -53,6 +53,7 @@ __device__ __forceinline__ float reciprocal(float s) {
 template <int GROUP, int VEC, int N>
 struct Row {
     static constexpr int kGroup = GROUP, kVec = VEC, kN = N, kValues = N * VEC;
+    static constexpr int kMaxE = GROUP * VEC * N;  // experts that fit
     // first of the VEC experts of this lane's q-th load
     static __device__ __forceinline__ int expert(int lane, int q) {
         return (q * GROUP + lane) * VEC;
@@ -208,6 +209,9 @@ __device__ __forceinline__ void join_sequence(const BalanceArgs &a, int b, Ready
     if (threadIdx.x == 0)
         a.loss[s] = (float)((double)a.alpha * a.E / ((double)a.K * len * len) * dot);
 }
+
+// Dynamic shared memory of a tile's block: the warps' sums and the counts.
+constexpr size_t balance_smem(int E) { return sizeof(float) * (BAL_WARPS + 1) * (size_t)E; }
 
 // One tile of tokens per block.  CLUSTER: the blocks are one cluster, and join the
 // crossing sequences themselves.
@@ -585,12 +589,6 @@ cudaError_t with_row(int E, F f) {
     return f(Row<32, 1, 32>{});
 }
 
-template <class Kern>
-cudaError_t allow_smem(Kern kern, size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
@@ -601,15 +599,22 @@ cudaError_t launch_balance_loss(const float *scores, const int32_t *topk_idx,
     BalanceArgs a{scores, topk_idx, offsets, n_seq, T, E, K, balance_tile(T, n_seq), alpha,
                   counts, prob, loss, part, part_n, status};
     const int tiles = T > 0 ? (T + a.tile - 1) / a.tile : 1;
-    const size_t smem = sizeof(float) * (size_t)E * (BAL_WARPS + 1);
+    const size_t smem = balance_smem(E);
     cudaError_t err = with_row(E, [&](auto row) {
         // up to BAL_CLUSTER tiles are one cluster and one launch (520 tokens of 40 experts:
         // 8.2 us a call, 10.3 with the second launch)
         const bool one = tiles > 1 && tiles <= BAL_CLUSTER;
         auto kern = one ? balance_tile_kernel<decltype(row), true>
                         : balance_tile_kernel<decltype(row), false>;
-        const cudaError_t e = allow_smem(kern, smem);
-        if (e != cudaSuccess) return e;
+        // Beside what the kernel declares (4352 bytes with the join, 128 without), rows of
+        // more than 658 experts pass the 48 KB that need no leave.  It is asked for
+        // the layout's largest E, whatever this call's: no call depends on another's.
+        constexpr size_t most = balance_smem(decltype(row)::kMaxE);
+        if (most > 40 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+            if (e != cudaSuccess) return e;
+        }
         if (one) return launch_dependent(kern, tiles, BAL_THREADS, smem, tiles, st, a);
         return launch_dependent(kern, tiles, BAL_THREADS, smem, 1, st, a);
     });
@@ -633,9 +638,8 @@ cudaError_t launch_route_backward(const float *scores, const int32_t *topk_idx,
                                    : (softplus ? route_backward_kernel<R, many, true>
                                                : route_backward_kernel<R, many, false>);
         constexpr int groups = GRAD_THREADS / R::kGroup;
+        static_assert(sizeof(float) * R::kMaxE * groups <= 32 * 1024);
         const size_t smem = d_topk_w ? sizeof(float) * (size_t)E * groups : 0;
-        const cudaError_t e = allow_smem(kern, smem);
-        if (e != cudaSuccess) return e;
         // consecutive tokens to a block, the same number to each of its groups: one wave
         // of blocks for long batches, a token a group for short ones
         const int64_t round = (int64_t)groups * grad_blocks<R>() * 148;

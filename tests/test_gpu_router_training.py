@@ -7,6 +7,11 @@ reciprocal and the product, p is off by at most 40 u. prob adds at most tile / 1
 lane, 1 + 16 across a block and tiles / 8 + 8 across blocks, all non-negative, so its relative error
 is the number of additions times u.
 """
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -571,3 +576,69 @@ def test_python_entry_points_refuse_wrong_tensors():
     with pytest.raises(moe.MoeError):
         moe.moe_route_backward(cfg_of(T, E, K, moe.MOE_ROUTER_HASH), s, idx, dw, None, None, None,
                                1.0, out)
+
+
+# ------------------------------------------------------------------ sizes that need more shared memory
+def child(call):
+    """Runs ``call``, a line of this module, in a process of its own: what an earlier call of this one
+    did to the kernels' settings must not matter."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"import tests.test_gpu_router_training as t; t.{call}"],
+                       cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def check_balance(T, E, K):
+    """Both of the loss's kernels at (T, E, K): one sequence, and some that cross tiles."""
+    cfg, alpha = cfg_of(T, E, K), 0.25
+    s, idx, _ = inputs(T, E, K)
+    for o in (None, SEQ["straddle"](T)):
+        n, p, loss, ws = balance(cfg, s, idx, offsets(o), alpha)
+        assert moe.moe_read_device_status(ws) == moe.MOE_OK
+        ref_n = R.counts(idx, o, E)
+        assert torch.equal(n.long(), ref_n)
+        ref_p, ref_loss = R.balance_loss(s.double(), ref_n, o, alpha, K)
+        bound = (40 + tile(T) / 16 + 2 + 17 + T / tile(T) / 8 + 9) * U
+        assert ((p.double() - ref_p).abs() <= bound * ref_p).all()
+        assert ((loss.double() - ref_loss).abs() <= (bound + 4 * U) * ref_loss).all()
+
+
+def balance_sizes():
+    for E in (655, 658, 659, 660, 704, 721, 722, 723, 724, 1023, 1024):  # ascending: no earlier call
+        for T in (20, 40, 1000, 1300):                                   # asked for more
+            check_balance(T, E, 4)
+
+
+def test_balance_loss_of_many_experts_in_a_fresh_process():
+    """68 bytes of shared memory an expert and what the kernels declare besides (4352 bytes where
+    the batch is one cluster) pass 48 KB from 659 experts on."""
+    child("balance_sizes()")
+
+
+def balance_from_two_threads():
+    """Sizes of one row layout, each in a thread of its own: neither call's setting is the other's."""
+    fails = []
+
+    def work(E):
+        try:
+            cfg = cfg_of(64, E, 2)
+            s, idx, _ = inputs(64, E, 2)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                torch.cuda.synchronize()
+                n, p, loss, ws = balance(cfg, s, idx, None, 0.25)
+                for _ in range(20000):
+                    moe.moe_balance_loss(cfg, s, idx, None, 0.25, n, p, loss, ws)
+            torch.cuda.synchronize()
+        except Exception as e:  # (for the test's own thread)
+            fails.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(E,)) for E in (732, 1024)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not fails, fails
+
+
+def test_balance_loss_from_two_threads():
+    child("balance_from_two_threads()")
