@@ -227,6 +227,11 @@ struct SmallDispatch {
     int32_t *counts, *offsets, *send, *send_tok, *perm_token, *inv_perm, *status;
 };
 
+// Its dynamic shared memory: the tokens' bits, the offsets, and the two send matrices.
+constexpr size_t small_dispatch_smem(int E, int G) {
+    return sizeof(uint32_t) * ((size_t)E * (DISPATCH_BLOCK / 32) + E + 1 + 2 * G * G);
+}
+
 __global__ void __launch_bounds__(DISPATCH_BLOCK)
 dispatch_int8_small_kernel(const SmallDispatch a) {
     constexpr int BLK = DISPATCH_BLOCK, WORDS = BLK / 32, KMAX = 32;
@@ -470,10 +475,13 @@ cudaError_t launch_dispatch_int8(const void *x, const int32_t *topk_idx, int T, 
     if (dispatch_int8_in_one(T, K)) {
         SmallDispatch a{q, topk_idx, T, E, G, counts, offsets, send, send_tok, perm_token, inv_perm,
                         status};
-        const size_t smem = sizeof(uint32_t) * ((size_t)E * (DISPATCH_BLOCK / 32) + E + 1 + 2 * G * G);
-        if (smem > 48 * 1024) {
+        // Beside the 192 bytes that the kernel declares, 48 KB need no leave.  It is
+        // asked for the largest E and G, whatever this call's: no call depends on another's.
+        const size_t smem = small_dispatch_smem(E, G);
+        if (smem > 40 * 1024) {
             const cudaError_t err = cudaFuncSetAttribute(
-                dispatch_int8_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                dispatch_int8_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                (int)small_dispatch_smem(1024, 64));
             if (err != cudaSuccess) return err;
         }
         return launch_dependent(dispatch_int8_small_kernel, T, DISPATCH_BLOCK, smem, 1, st, a);

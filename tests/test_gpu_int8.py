@@ -1,4 +1,8 @@
 """The int8 experts on the GPU: codes and scales bit for bit, the products against 64 bits."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -481,3 +485,26 @@ def test_short_pair_kernels_behind_one_another(d, d_ff):
         assert torch.equal(y, y2) and torch.equal(sh, sh2)
         assert moe.moe_read_device_status(ws) == moe.MOE_OK
         check_ffn(cfg, xq, xs, offsets, w, x, y, sh)
+
+
+# ------------------------------------------------------------------ sizes that need more shared memory
+def dispatch_sizes():
+    for T, E, G, K, M in ((118, 590, 59, 4, 2), (118, 649, 59, 4, 2), (256, 1024, 64, 8, 4)):
+        cfg, g = config(T, 64, E, K, 64, G=G, M=M), gen(E)
+        x, idx = torch.randn(T, 64, device=DEV, generator=g).bfloat16(), routing(T, E, K, g)
+        o, q, s = dispatch(cfg, x, idx, moe.alloc_workspace(cfg))
+        plain = {k: torch.empty_like(v) for k, v in o.items()}
+        moe.moe_dispatch(cfg, None, idx, *plain.values(), None, moe.alloc_workspace(cfg))
+        assert all(torch.equal(o[k], plain[k]) for k in o), (E, G)
+        rq, rs = R.quantize(x.float())
+        tok = o["perm_token"].long()
+        assert torch.equal(q.double(), rq[tok]) and torch.equal(s.double(), rs[tok, 0])
+
+
+def test_dispatch_int8_of_many_experts_and_groups_in_a_fresh_process():
+    """590 experts in 59 groups take 49092 bytes of shared memory, which with the 192 that the
+    kernel declares are more than 48 KB; nothing before this call asked for more."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", "import tests.test_gpu_int8 as t; t.dispatch_sizes()"],
+                       cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
