@@ -136,7 +136,7 @@ moe_status check_device() {
     return v == 1 ? MOE_OK : MOE_ERR_NO_DEVICE;
 }
 
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : cuda_failed(); }
 
 // Affinity router + node-limited top-K.  Up to 256 experts (G <= 32, E/G <= 32)
 // one fused kernel keeps the affinities on chip and writes `scores` only when
@@ -255,7 +255,7 @@ moe_status moe_read_device_status(const void *ws, int32_t *host_status, void *st
     if (st) return st;
     cudaStream_t s = as_stream(stream);
     if (cudaMemcpyAsync(host_status, ws, sizeof(int32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return cuda_status(cudaStreamSynchronize(s));
 }
 
@@ -421,7 +421,7 @@ moe_status moe_dispatch_fp8(const moe_config *c, const void *x, const int32_t *t
                   at<int32_t>(ws, L.send_part), at<int32_t>(ws, L.sendtok_part)};
     if (launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send, send_tok,
                         perm_token, inv_perm, nullptr, dw, at<int32_t>(ws, L.status), s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return cuda_status(launch_gather_fp8(x, inv_perm, c->T, c->d, c->K, x_perm_q, x_scale, s));
 }
 
@@ -607,11 +607,11 @@ static moe_status forward_impl(const moe_config *c, const void *x, const float *
     StageRange stage("moe.route");
     if (c->router == MOE_ROUTER_HASH) {
         if (launch_hash_route(token_ids, c->T, c->E, c->G, c->K, c->M, topk_idx, topk_w, s))
-            return MOE_ERR_CUDA;
+            return cuda_failed();
     } else {
         if (route_affinity(*c, x, router_w, logit_offset, bias, topk_idx, topk_w, nullptr, ws, L,
                            s))
-            return MOE_ERR_CUDA;
+            return cuda_failed();
     }
     stage.next("moe.dispatch");
     DispatchWs dw{at<int32_t>(ws, L.hist_t), at<int32_t>(ws, L.base_t),
@@ -629,9 +629,9 @@ static moe_status forward_impl(const moe_config *c, const void *x, const float *
     float *x_scale = reinterpret_cast<float *>(x_perm_q + (size_t)c->T * c->K * c->d);
     if (launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets, send, send_tok,
                         perm_token, inv_perm, fp8 ? nullptr : x_perm, dw, status, s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     if (fp8 && launch_gather_fp8(x, inv_perm, c->T, c->d, c->K, x_perm_q, x_scale, s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     stage.next("moe.expert_ffn");
     FfnArgs a{};
     a.T = c->T; a.d = c->d; a.E = c->E; a.K = c->K; a.d_ff = c->d_ff;
@@ -645,7 +645,7 @@ static moe_status forward_impl(const moe_config *c, const void *x, const float *
     a.packed = packed;
     a.status = status;
     a.timeout_ns = kWaitTimeoutNs;
-    if (launch_expert_ffn(a, s)) return MOE_ERR_CUDA;
+    if (launch_expert_ffn(a, s)) return cuda_failed();
     stage.next("moe.combine");
     return cuda_status(launch_combine(y_perm, inv_perm, topk_w, y_sh, c->T, c->d, c->K,
                                       (int64_t)c->T * c->K, out, s));
@@ -1071,10 +1071,10 @@ moe_status moe_ipc_get_handle(const void *dev_ptr, void *handle) {
     // allocator may place a buffer inside a larger one): send the offset too
     CUdeviceptr base = 0;
     size_t bytes = 0;
-    if (!ipc_addr_range(dev_ptr, &base, &bytes)) return MOE_ERR_CUDA;
+    if (!ipc_addr_range(dev_ptr, &base, &bytes)) return cuda_failed();
     cudaIpcMemHandle_t h;
     if (cudaIpcGetMemHandle(&h, reinterpret_cast<void *>(base)) != cudaSuccess)
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     static_assert(sizeof(h) + sizeof(uint64_t) == MOE_IPC_HANDLE_BYTES, "IPC handle size");
     const uint64_t off = reinterpret_cast<uintptr_t>(dev_ptr) - (uintptr_t)base;
     std::memcpy(handle, &h, sizeof(h));
@@ -1208,12 +1208,12 @@ moe_status moe_quantize_weights_int8(const moe_config *c, const void *w_gate, co
     if (launch_quantize_rows_bf16(w_gate, up_rows, c->d, out->w_gate, out->w_gate_scale, s) ||
         launch_quantize_rows_bf16(w_up, up_rows, c->d, out->w_up, out->w_up_scale, s) ||
         launch_quantize_rows_bf16(w_down, down_rows, c->d_ff, out->w_down, out->w_down_scale, s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     if (c->n_shared == 0) return MOE_OK;
     const int64_t sh_rows = (int64_t)c->n_shared * c->d_ff_shared;
     if (launch_quantize_rows_bf16(ws_gate, sh_rows, c->d, out->ws_gate, out->ws_gate_scale, s) ||
         launch_quantize_rows_bf16(ws_up, sh_rows, c->d, out->ws_up, out->ws_up_scale, s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return cuda_status(launch_quantize_joint_bf16(ws_down, c->n_shared, c->d, c->d_ff_shared,
                                                   out->ws_down, out->ws_down_scale, s));
 }
@@ -1268,7 +1268,7 @@ moe_status moe_expert_ffn_int8(const moe_config *c, const int8_t *x_perm_q, cons
     if (c->n_shared > 0 &&
         launch_quantize_rows_bf16(x, c->T, c->d, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_q_scale),
                                   s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     return cuda_status(ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_shared,
                                 c->n_shared > 0, ws, L, s));
 }
@@ -1312,10 +1312,10 @@ moe_status moe_forward_int8(const moe_config *c, const void *x, const float *rou
     StageRange stage("moe.route");
     if (c->router == MOE_ROUTER_HASH) {
         if (launch_hash_route(token_ids, c->T, c->E, c->G, c->K, c->M, topk_idx, topk_w, s))
-            return MOE_ERR_CUDA;
+            return cuda_failed();
     } else if (route_affinity(*c, x, router_w, logit_offset, bias, topk_idx, topk_w, nullptr, ws, L,
                               s)) {
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     }
     stage.next("moe.dispatch");
     DispatchWs dw{at<int32_t>(ws, L.hist_t), at<int32_t>(ws, L.base_t),
@@ -1330,12 +1330,12 @@ moe_status moe_forward_int8(const moe_config *c, const void *x, const float *rou
                              shared ? at<int8_t>(ws, L8.x_q) : nullptr,
                              shared ? at<float>(ws, L8.x_q_scale) : nullptr, dw,
                              at<int32_t>(ws, L.status), s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     stage.next("moe.expert_ffn");
     // (the one-kernel dispatch also writes the offsets: nothing may be read ahead of it)
     if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, !dispatch_int8_in_one(c->T, c->K),
                  ws, L8, s))
-        return MOE_ERR_CUDA;
+        return cuda_failed();
     stage.next("moe.combine");
     return cuda_status(launch_combine(y_perm, inv_perm, topk_w, y_sh, c->T, c->d, c->K,
                                       (int64_t)c->T * c->K, out, s));

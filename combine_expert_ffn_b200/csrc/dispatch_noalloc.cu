@@ -94,7 +94,7 @@ extern "C" moe_status moe_dispatch_noalloc(const moe_config *c, const void *x,
         major != 10)
         return MOE_ERR_NO_DEVICE;
     void *base = nullptr;
-    if (scratch_address(&base) != cudaSuccess) return MOE_ERR_CUDA;
+    if (scratch_address(&base) != cudaSuccess) return cuda_failed();
     char *b = static_cast<char *>(base);
     DispatchWs dw{reinterpret_cast<int32_t *>(b + L.hist_t), reinterpret_cast<int32_t *>(b + L.base_t),
                   reinterpret_cast<int32_t *>(b + L.send_part),
@@ -103,5 +103,5 @@ extern "C" moe_status moe_dispatch_noalloc(const moe_config *c, const void *x,
     cudaError_t e = launch_dispatch(x, topk_idx, c->T, c->d, c->E, c->G, c->K, counts, offsets,
                                     send, send_tok, perm_token, inv_perm, x_perm, dw, status,
                                     static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return e == cudaSuccess ? MOE_OK : cuda_failed();
 }

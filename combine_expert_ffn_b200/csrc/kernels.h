@@ -14,6 +14,14 @@ namespace moe {
 // Counts one kernel launch (process-wide, for moe_launch_count()).
 void count_launch();
 
+// The status of an entry point whose CUDA call failed.  The runtime keeps such an error, and
+// the next launcher that asks for the last one would report it for a call that was right:
+// it is taken here, with the call that it belongs to.
+inline moe_status cuda_failed() {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
+
 // Launches and counts kern as a dependent of the kernel before it on the stream, in
 // clusters of `cluster` blocks: it may be placed while that kernel still runs, and
 // waits for it by dependency_wait() -- in every block, since what follows on the

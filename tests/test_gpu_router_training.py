@@ -7,6 +7,7 @@ reciprocal and the product, p is off by at most 40 u. prob adds at most tile / 1
 lane, 1 + 16 across a block and tiles / 8 + 8 across blocks, all non-negative, so its relative error
 is the number of additions times u.
 """
+import ctypes as C
 import os
 import subprocess
 import sys
@@ -642,3 +643,32 @@ def balance_from_two_threads():
 
 def test_balance_loss_from_two_threads():
     child("balance_from_two_threads()")
+
+
+def right_call_after_a_refused_launch():
+    """A launch that CUDA refuses on the host (on the legacy stream while a stream that it would have
+    to wait for is capturing) is that call's error and no other's."""
+    T, E, K = 64, 16, 2
+    cfg = cfg_of(T, E, K)
+    s, idx, g = inputs(T, E, K)
+    n, p, loss, ws = balance(cfg, s, idx, None, 1.0)
+    g, y, inv, w = combine_inputs(T, 64, K)
+    out, want = torch.empty_like(g), torch.empty_like(g)
+    moe.moe_combine(cfg, y, inv, w, None, want)
+    torch.cuda.synchronize()
+    path = next(line.split()[-1] for line in open("/proc/self/maps") if "libcudart" in line)
+    rt, stream, graph = C.CDLL(path), C.c_void_p(), C.c_void_p()
+    assert rt.cudaStreamCreate(C.byref(stream)) == 0
+    assert rt.cudaStreamBeginCapture(stream, 0) == 0
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_balance_loss(cfg, s, idx, None, 1.0, n, p, loss, ws, stream=0)
+    assert e.value.status == moe.MOE_ERR_CUDA
+    assert rt.cudaStreamEndCapture(stream, C.byref(graph)) != 0  # the capture is lost
+    rt.cudaGetLastError()
+    moe.moe_combine(cfg, y, inv, w, None, out)  # raises where the error above is still there
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_a_refused_launch_is_not_the_next_calls_error():
+    child("right_call_after_a_refused_launch()")
