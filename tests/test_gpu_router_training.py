@@ -672,3 +672,38 @@ def right_call_after_a_refused_launch():
 
 def test_a_refused_launch_is_not_the_next_calls_error():
     child("right_call_after_a_refused_launch()")
+
+
+# ------------------------------------------------------------------ digits of the router gradient
+def gate_bound(s, idx, dw, router):
+    """Element bound of the gates' gradient r w_j (dw_j - m), m = sum_k dw_k w_k, that does not scale
+    with the largest gradient.  Taken off every dw is that of a gate whose weight is the largest (by
+    2^-18 of it at most), so at least 1 / K: its size is at most K A, A = sum_k |dw_k| w_k, and each
+    of 60 roundings (7 a sum, the slope's 20 among them) is one of |dw_j| or of at most (K + 1) A."""
+    w, K = R.gates(s.double(), idx), idx.shape[1]
+    a = (w * dw.double().abs()).sum(1, keepdim=True)
+    b = torch.zeros(s.shape, dtype=torch.float64, device=DEV)
+    b.scatter_add_(1, idx.long(), w * (dw.double().abs() + 1.001 * (K + 1) * a))
+    return 60 * U * b + 1e-30
+
+
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("T,E,K", [(64, 16, 4), (64, 64, 8), (50, 64, 6), (40, 256, 8), (33, 256, 17),
+                                   (21, 24, 12), (20, 30, 9), (20, 1024, 32), (9, 254, 31), (7, 40, 1)])
+def test_route_backward_of_a_small_gate_with_a_large_gradient(T, E, K, router):
+    """One gate of each token, in every slot in turn, is 1e-3 to 1e-12 of the others and has a
+    gradient of the inverse size: it hardly enters the others' gradients, which keep their digits."""
+    cfg = cfg_of(T, E, K, router)
+    s, idx, g = inputs(T, E, K, router)
+    t = torch.arange(T, device=DEV)
+    slot = t % K
+    small = 10.0 ** -(3 + 9 * torch.rand(T, device=DEV, generator=g))
+    s[t, idx[t, slot].long()] *= small
+    dw = torch.randn(T, K, device=DEV, generator=g)
+    dw[t, slot] /= small
+    out = torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(cfg, s, idx, dw, None, None, None, 0.0, out)
+    ref = reference(s, idx, dw, None, None, None, 0.0, router)
+    off = (out.double() - ref).abs()
+    bound = gate_bound(s, idx, dw, router)
+    assert (off <= bound).all(), float((off / bound).max())
