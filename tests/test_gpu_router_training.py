@@ -707,3 +707,27 @@ def test_route_backward_of_a_small_gate_with_a_large_gradient(T, E, K, router):
     off = (out.double() - ref).abs()
     bound = gate_bound(s, idx, dw, router)
     assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("router", [0, 1])
+@pytest.mark.parametrize("T,E,K", [(96, 64, 6), (70, 256, 8), (33, 30, 3), (40, 1024, 4), (24, 1022, 2)])
+@pytest.mark.parametrize("seq", ["none", "padded", "singles", "straddle"])
+def test_route_backward_of_counts_summed_over_ranks(T, E, K, seq, router):
+    """Counts of a step's eight ranks: large and nearly equal, their mean far from this rank's
+    K N / E.  What is left of them beside their own mean is the gradient, to fp32's digits of it."""
+    cfg, alpha = cfg_of(T, E, K, router), 1.0
+    s, idx, g = inputs(T, E, K, router)
+    o = SEQ[seq](T)
+    n = 8 * R.counts(idx, o, E) + 100_000
+    n += torch.randint(0, 50, n.shape, device=DEV, generator=g)
+    dl = torch.randn(n.shape[0], device=DEV, generator=g)
+    out = torch.empty(T, E, device=DEV)
+    moe.moe_route_backward(cfg, s, idx, None, offsets(o), n.int(), dl, alpha, out)
+    pull = pull_of(n, o, dl, alpha, K, T, E)
+    S = s.double()
+    p = S / S.sum(1, keepdim=True)
+    ref = p * (pull - (pull * p).sum(1, keepdim=True))
+    ref *= -torch.expm1(-S * S) / (2 * S * S) if router else 1 - S
+    off = (out.double() - ref).abs()
+    bound = route_bound(s, idx, None, pull, router)
+    assert (off <= bound).all(), float((off / bound).max())
