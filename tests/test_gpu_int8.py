@@ -508,3 +508,31 @@ def test_dispatch_int8_of_many_experts_and_groups_in_a_fresh_process():
     r = subprocess.run([sys.executable, "-c", "import tests.test_gpu_int8 as t; t.dispatch_sizes()"],
                        cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ the rows of bad segments
+@pytest.mark.parametrize("n_shared", [0, 1])
+def test_bad_segments_are_neither_computed_nor_written(n_shared):
+    """Segments that leave the buffer or have a negative length are empty; the others are computed,
+    and rows of no valid segment stay as they were."""
+    cfg, xq, xs, offsets, w, x = ffn_inputs((50, 128, 4, 1, 64, n_shared, 64 * n_shared, 0.0))
+    for off in ([0, 10, 20, 30, 51], [-3, 10, 20, 30, 50], [0, 2 ** 31 - 1, 20, 30, 50],
+                [12, 12, 5, 20, -1], [0, 10, 5, 20, 50]):
+        y, sh, ws = run_ffn(cfg, xq, xs, torch.tensor(off, dtype=torch.int32, device=DEV), w, x)
+        assert moe.moe_read_device_status(ws) == moe.MOE_ERR_DEVICE_FAULT, off
+        owners = torch.zeros(50, dtype=torch.int64, device=DEV)
+        valid = [(e, lo, hi) for e, (lo, hi) in enumerate(zip(off, off[1:])) if 0 <= lo <= hi <= 50]
+        for _, lo, hi in valid:
+            owners[lo:hi] += 1
+        for e, lo, hi in valid:
+            one = owners[lo:hi] == 1  # a row of two segments has either's value
+            if hi == lo or not one.any():
+                continue
+            some = {k: v if k.startswith("ws_") else v[e:e + 1] for k, v in w.items()}
+            want, room = R.ffn(config(50, 128, 1, 1, 64), xq[lo:hi], xs[lo:hi], [0, hi - lo], some,
+                               None)[0]
+            assert ((y[lo:hi].double() - want).abs() <= room)[one].all(), (off, e)
+        assert y[owners == 0].isnan().all() and not y[owners > 0].isnan().any(), off
+        if n_shared:
+            want, room = R.ffn(cfg, xq, xs, [0, 50, 50, 50, 50], w, x)[1]
+            assert ((sh.double() - want).abs() <= room).all()
