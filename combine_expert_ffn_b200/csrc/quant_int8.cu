@@ -1,8 +1,11 @@
 // quant_int8.cu -- rows to signed 8-bit codes with one fp32 scale per row:
-//   s = amax / 127 (fp32 division),  q = rint(x / s) (fp32 division, nearest even)
-// so that x ~ s q and the row's largest magnitude is +-127.  A row of zeros has
-// s = 0 and codes 0; a row that holds a NaN or an infinity has s = NaN (and
-// codes 0), so that whatever is computed from it is NaN as it would be from x.
+//   s = amax / 127 (fp32 division)
+//   q = rint(x / s) (fp32 division, nearest even)               bf16 rows
+//   q = rint(x * fp32(1 / s)) (exact product, nearest even)     fp32 rows: h
+// so that x ~ s q and the row's largest magnitude is +-127.  (The two differ only where
+// x / s lies within 2^-22 of its size of a half.)  A row of zeros has s = 0 and
+// codes 0; a row that holds a NaN or an infinity has s = NaN (and codes 0), so that
+// whatever is computed from it is NaN as it would be from x.
 //
 // Used for the dispatch payload (a token's codes go to its K permuted rows), the
 // shared experts' input, the SwiGLU intermediate and, once at load, the
@@ -65,8 +68,9 @@ __device__ __forceinline__ uint32_t code(float x, float s) {
 // of a normal row) to be told apart: |x| = half gets at_half, 63.25 or 63.75 as the
 // division says.
 // Rows in fp32 are the library's own h, whose 24-bit rounding moves codes that near a
-// half either way already: they take the product as it is (65536 rows of 2048 values:
-// 144 us with the check, 98 without, as long as a copy of the bytes takes).
+// half either way already: their codes are the product's, by definition (65536 rows of
+// 2048 values with the division's: 144 us, without 98, as long as a copy of the bytes takes).
+// Where 1 / s is no normal number they are the division's.
 template <bool TIE, int N>
 __device__ __forceinline__ bool codes(const float (&x)[N], float inv, float half, float at_half,
                                       uint32_t (&c)[N / 4]) {
@@ -75,9 +79,13 @@ __device__ __forceinline__ bool codes(const float (&x)[N], float inv, float half
     float far = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float t = TIE && fabsf(x[i]) == half ? copysignf(at_half, x[i]) : x[i] * inv;
+        if (!TIE) {
+            b[i] = __float_as_uint(fmaf(x[i], inv, kMagic));
+            continue;
+        }
+        const float t = fabsf(x[i]) == half ? copysignf(at_half, x[i]) : x[i] * inv;
         const float r = t + kMagic;
-        if (TIE) far = fmaxf(far, fmaf(fabsf(t), 0x1p-22f, fabsf(t - (r - kMagic))));
+        far = fmaxf(far, fmaf(fabsf(t), 0x1p-22f, fabsf(t - (r - kMagic))));
         b[i] = __float_as_uint(r);
     }
 #pragma unroll

@@ -551,7 +551,10 @@ MOE_API moe_status moe_dispatch_int8(const moe_config *cfg, const void *x,
  * Expert FFN on int8 codes.  Per expert segment, with row scale sx and channel
  * scales sg, su, sd:
  *   g = sx sg (Xq Wgq^T),  u = sx su (Xq Wuq^T),  h = SiLU(g) u     in fp32
- *   (Hq, sh) = the codes and scale of each row of h
+ *   (Hq, sh) = the codes and scale of each row of h: sh as above, but
+ *              Hq = rint(h * fp32(1 / sh)) of the exact product (nearest even), which
+ *              is rint(h / sh) but where h / sh lies within 2^-22 of its size of a
+ *              half (the division's where 1 / sh is no normal fp32 number)
  *   y = bf16(sh sd (Hq Wdq^T))
  * The products are exact 32-bit integer sums on the tensor cores.  The shared
  * experts quantize each row of x and run as one expert of width

@@ -536,3 +536,41 @@ def test_bad_segments_are_neither_computed_nor_written(n_shared):
         if n_shared:
             want, room = R.ffn(cfg, xq, xs, [0, 50, 50, 50, 50], w, x)[1]
             assert ((sh.double() - want).abs() <= room).all()
+
+
+# ------------------------------------------------------------------ the codes of h
+def test_codes_of_h_are_those_of_the_product_with_the_reciprocal():
+    """h's codes by their rule, rint(h * fp32(1 / s)) of the exact product, where a division gives
+    others: rows whose h lies on every half between two codes, for scales of inexact reciprocal.
+    g = 128, whose SiLU is 128 itself (e^-128 adds nothing to 1), u = j m with whole j and m, so
+    h = 128 j m exactly; its largest is 128 * 254 m, s = 256 m, and h / s = j / 2.  w_down copies
+    code c to channel c, in units."""
+    d = d_ff = 512
+    ms = [m for m in range(3, 128, 2)]
+    T = len(ms)
+    cfg = config(T, d, 1, 1, d_ff)
+    j = torch.cat([torch.arange(-254, 255), torch.tensor([254, 1, -1])])  # 512 values, 254 among them
+    xq = torch.zeros(T, d, dtype=torch.int8)
+    xq[:, 0] = xq[:, 1] = torch.tensor(ms)
+    xq[:, 2] = 1
+    up, gate = torch.zeros(1, d_ff, d, dtype=torch.int8), torch.zeros(1, d_ff, d, dtype=torch.int8)
+    up[0, :, 0] = torch.div(j, 2, rounding_mode="floor")
+    up[0, :, 1] = j - torch.div(j, 2, rounding_mode="floor")
+    gate[0, :, 2] = 64
+    one = torch.ones(1, d_ff, device=DEV)
+    w = {"w_gate": gate.to(DEV), "w_up": up.to(DEV),
+         "w_down": torch.eye(d, dtype=torch.int8, device=DEV)[None].contiguous(),
+         "w_gate_scale": 2 * one, "w_up_scale": one.clone(), "w_down_scale": torch.ones(1, d, device=DEV)}
+    off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    y, _, ws = run_ffn(cfg, xq.to(DEV), torch.ones(T, device=DEV), off, w, x)
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    m = torch.tensor(ms, dtype=torch.float64)[:, None]
+    h, s = 128 * j.double() * m, 256 * m
+    inv = (1 / s).float().double()               # fp32(1 / s): 53 bits first, which is no tie of 24
+    want = (h * inv).round()                     # 24 + 24 bits: exact in 64
+    divided = (h / s).round()
+    assert int((want != divided).sum()) > 1000   # the two rules differ here
+    # y = bf16(code * s), an 8-bit code times s and one rounding: the nearest code is the code
+    got = (y.double().cpu() / s).round()
+    assert torch.equal(got, want)
