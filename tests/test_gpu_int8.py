@@ -574,3 +574,56 @@ def test_codes_of_h_are_those_of_the_product_with_the_reciprocal():
     # y = bf16(code * s), an 8-bit code times s and one rounding: the nearest code is the code
     got = (y.double().cpu() / s).round()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ what another stream writes
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [100, 300])
+def test_operands_that_another_stream_writes(T, captured):
+    """Every operand of the dispatch and of the experts -- offsets and weights too, which a product
+    may read while the kernel before it still runs -- comes from another stream, which the calls'
+    stream waits for between two rounds of calls; eager, and as the branches of a graph."""
+    cfg, xq, xs, offsets, w, x = ffn_inputs((T, 192, 12, 4, 320, 1, 128, 0.0))
+    _, xq2, xs2, offsets2, w2, x2 = ffn_inputs((T, 192, 12, 4, 320, 1, 128, 0.0), seed=77)
+    g = gen(5)
+    idx, idx2 = routing(T, 12, 4, g), routing(T, 12, 4, g)
+    ws = [moe.alloc_int8_workspace(cfg) for _ in range(2)]
+    want = (*run_ffn(cfg, xq2, xs2, offsets2, w2, x2)[:2], *dispatch(cfg, x2, idx2, ws[0]))
+    weights = moe.Int8Weights(**w)
+    pairs = [(xq, xq2), (xs, xs2), (offsets, offsets2), (x, x2), (idx, idx2)] + [(w[k], w2[k]) for k in w]
+    y, sh = torch.empty(xq.shape, dtype=torch.bfloat16, device=DEV), torch.empty_like(x)
+    first = [a.clone() for a, _ in pairs]
+    o, q, s = dispatch(cfg, x, idx, ws[0])
+    side = torch.cuda.Stream()
+
+    def calls():
+        moe.moe_dispatch_int8(cfg, x, idx, *o.values(), q, s, ws[1])
+        moe.moe_expert_ffn_int8(cfg, xq, xs, offsets, weights, y, x, sh, ws[0])
+
+    def run():
+        here = torch.cuda.current_stream()
+        calls()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+            for a, b in pairs:
+                a.copy_(b)
+        here.wait_stream(side)
+        calls()
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(3):
+        for (a, _), b in zip(pairs, first):
+            a.copy_(b)
+        y.fill_(float("nan"))
+        q.fill_(77)
+        graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(sh, want[1])
+        assert all(torch.equal(o[k], want[2][k]) for k in o)
+        assert torch.equal(q, want[3]) and torch.equal(s, want[4])
+    for wsp in ws:
+        assert moe.moe_read_device_status(wsp) == moe.MOE_OK

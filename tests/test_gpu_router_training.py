@@ -731,3 +731,56 @@ def test_route_backward_of_counts_summed_over_ranks(T, E, K, seq, router):
     off = (out.double() - ref).abs()
     bound = route_bound(s, idx, None, pull, router)
     assert (off <= bound).all(), float((off / bound).max())
+
+
+# ------------------------------------------------------------------ what another stream writes
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [200, 3000])
+def test_affinities_that_another_stream_writes(T, captured):
+    """Loss and gradient behind an event of the stream that writes all they read, with a round of
+    the same calls right before it; eager, and as the branches of a graph."""
+    E, K, alpha = 64, 6, 0.5
+    cfg = cfg_of(T, E, K)
+    s, idx, g = inputs(T, E, K)
+    s2, idx2, _ = inputs(T, E, K, seed=9)
+    dw, dw2 = (torch.randn(T, K, device=DEV, generator=g) for _ in range(2))
+    o, o2 = offsets([0, T // 3, T]), offsets([0, T // 2, T - 5])
+    dl, dl2 = torch.tensor([1.0, 2.0], device=DEV), torch.tensor([3.0, -1.0], device=DEV)
+    ws, fault = moe.alloc_workspace(cfg), torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def calls(s, idx, dw, o, dl, out):
+        moe.moe_balance_loss(cfg, s, idx, o, alpha, *out[:3], ws)
+        moe.moe_route_backward(cfg, s, idx, dw, o, out[0], dl, alpha, out[3], fault)
+
+    def outs():
+        return (torch.full((2, E), -7, dtype=torch.int32, device=DEV), torch.zeros(2, E, device=DEV),
+                torch.zeros(2, device=DEV), torch.zeros(T, E, device=DEV))
+
+    want, out = outs(), outs()
+    calls(s2, idx2, dw2, o2, dl2, want)
+    pairs = [(s, s2), (idx, idx2), (dw, dw2), (o, o2), (dl, dl2)]
+    first = [a.clone() for a, _ in pairs]
+    side = torch.cuda.Stream()
+
+    def run():
+        here = torch.cuda.current_stream()
+        calls(s, idx, dw, o, dl, out)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+            for a, b in pairs:
+                a.copy_(b)
+        here.wait_stream(side)
+        calls(s, idx, dw, o, dl, out)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(3):
+        for (a, _), b in zip(pairs, first):
+            a.copy_(b)
+        graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK and int(fault) == 0
