@@ -246,6 +246,15 @@ class _Call:
                 return t.data_ptr()
         raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
 
+    def weights(self, w):
+        """A reference to an Int8Weights whose tensors fit the configuration; None passes."""
+        if w is None:
+            return None
+        if not isinstance(w, Int8Weights):
+            raise MoeError(self.fn, MOE_ERR_INVALID_ARG)
+        w.check(self.fn, self.c)
+        return C.byref(w)
+
     def ws(self, ws):
         """(device pointer, bytes) of a workspace tensor."""
         if ws is None:
@@ -433,12 +442,11 @@ def moe_quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate, ws_up, ws_down
                               stream=None) -> None:
     k = _Call("moe_quantize_weights_int8", cfg)
     c = k.c
-    weights.check(k.fn, c)
+    w8 = k.weights(weights)
     n, ns = c.E * c.d_ff * c.d, c.n_shared * c.d_ff_shared * c.d
     ptrs = [k.t(w, torch.bfloat16, n) for w in (w_gate, w_up, w_down)]
     ptrs += [k.t(w, torch.bfloat16, ns) for w in (ws_gate, ws_up, ws_down)]
-    _ok(k.fn, _lib.moe_quantize_weights_int8(C.byref(c), *ptrs, C.byref(weights),
-                                             k.stream(stream)))
+    _ok(k.fn, _lib.moe_quantize_weights_int8(C.byref(c), *ptrs, w8, k.stream(stream)))
 
 
 def quantize_weights_int8(cfg, w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None,
@@ -479,10 +487,10 @@ def moe_expert_ffn_int8(cfg, x_perm_q, x_scale, offsets, weights, y_perm, x, y_s
     k = _Call("moe_expert_ffn_int8", cfg)
     c, t, bf16 = k.c, k.t, torch.bfloat16
     rows = c.T * c.K
-    weights.check(k.fn, c)
+    w8 = k.weights(weights)
     _ok(k.fn, _lib.moe_expert_ffn_int8(
         C.byref(c), t(x_perm_q, torch.int8, rows * c.d), t(x_scale, torch.float32, rows),
-        t(offsets, torch.int32, c.E + 1), C.byref(weights), t(y_perm, bf16, rows * c.d),
+        t(offsets, torch.int32, c.E + 1), w8, t(y_perm, bf16, rows * c.d),
         t(x, bf16, c.T * c.d), t(y_shared, bf16, c.T * c.d), *k.ws(ws), k.stream(stream)))
 
 
@@ -493,11 +501,11 @@ def moe_forward_int8(cfg, x, router_w, logit_offset, bias, weights, out, topk_id
     k = _Call("moe_forward_int8", cfg)
     c, t, i32, f32 = k.c, k.t, torch.int32, torch.float32
     rows, groups = c.T * c.K, c.G * c.G
-    weights.check(k.fn, c)
+    w8 = k.weights(weights)
     _ok(k.fn, _lib.moe_forward_int8(
         C.byref(c), t(x, torch.bfloat16, c.T * c.d), t(router_w, f32, c.E * c.d),
         t(logit_offset, f32, c.E), t(bias, f32, c.E), t(token_ids, torch.int64, c.T),
-        C.byref(weights), t(out, torch.bfloat16, c.T * c.d), t(topk_idx, i32, rows),
+        w8, t(out, torch.bfloat16, c.T * c.d), t(topk_idx, i32, rows),
         t(topk_w, f32, rows), t(counts, i32, c.E), t(offsets, i32, c.E + 1),
         t(send, i32, groups), t(send_tok, i32, groups), *k.ws(ws), k.stream(stream)))
 

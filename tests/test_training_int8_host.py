@@ -233,3 +233,14 @@ def test_python_layer_refuses_host_tensors_and_wrong_types(moe):
         moe.Int8Weights(w_gate=torch.zeros(4))
     with pytest.raises(TypeError):
         moe.Int8Weights(w_gate_scale=torch.zeros(4, 4).t())
+
+
+def test_python_layer_refuses_weights_that_are_missing_or_of_another_type(moe):
+    c = cfg(moe)
+    for w in (None, {}, torch.zeros(4, dtype=torch.int8)):
+        assert refused(moe, moe.moe_quantize_weights_int8, c, P, P, P, P, P, P, w, 0) == \
+            moe.MOE_ERR_INVALID_ARG
+        assert refused(moe, moe.moe_expert_ffn_int8, c, P, P, P, w, P, P, P, None, 0) == \
+            moe.MOE_ERR_INVALID_ARG
+        assert refused(moe, moe.moe_forward_int8, c, P, P, None, None, w, P, None, None, None, None,
+                       None, None, None, 0) == moe.MOE_ERR_INVALID_ARG
