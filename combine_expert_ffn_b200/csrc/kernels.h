@@ -73,7 +73,12 @@ bool tensor_map_3d_u8(CUtensorMap *m, const void *base, uint64_t n_mat, uint64_t
 // two byte tensors [n_mat, rows, cols], the second `gap` bytes (below 2^40) behind the
 // first, as one of five dimensions (column, row in group, first or second, group,
 // matrix): a box brings box_groups groups of rows of both, the two in turn, with
-// 128-byte swizzle
+// 128-byte swizzle.  The strides keep the encoder's stated limits (multiples of 16,
+// below 2^40), but do not nest as in its example of a padded array, where each is the one
+// before times an extent: gap stands before the group's stride, as the strides of
+// any view with swapped dimensions do.  An address is the base plus coordinate times
+// stride, dimension by dimension, and each coordinate is checked against its own extent,
+// so every byte that a box brings lies in one of the two tensors.
 bool tensor_map_pair_u8(CUtensorMap *m, const void *first, uint64_t gap, uint64_t n_mat,
                         uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t group,
                         uint32_t box_groups);
