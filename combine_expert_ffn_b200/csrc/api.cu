@@ -1333,7 +1333,7 @@ moe_status moe_forward_int8(const moe_config *c, const void *x, const float *rou
         return cuda_failed();
     stage.next("moe.expert_ffn");
     // (the one-kernel dispatch also writes the offsets: nothing may be read ahead of it)
-    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, !dispatch_int8_in_one(c->T, c->K),
+    if (ffn_int8(*c, x_perm_q, x_scale, offsets, *w, y_perm, y_sh, !dispatch_int8_in_one(c->T),
                  ws, L8, s))
         return cuda_failed();
     stage.next("moe.combine");

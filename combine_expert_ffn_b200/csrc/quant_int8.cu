@@ -225,9 +225,9 @@ quantize_rows_kernel(const QuantArgs a) {
 // token.  Every block builds the plan for itself -- a bit for each (expert, token), whose
 // counts over all tokens, scanned over the experts, are the offsets, and over the tokens
 // below its own the ranks -- and then writes its token's codes to its K rows; block 0
-// writes what belongs to the batch.  The ids (at most 4096) come from L2 for each block,
+// writes what belongs to the batch.  The ids (at most 8192) come from L2 for each block,
 // which is less than the two launches it saves: 1, 128 and 256 tokens of 7168, K = 8, 256
-// experts take 5.8, 7.0 and 9.3 us, the plan's two kernels and the gather 12.7, 15.5 and 18.8.
+// experts take 5.6, 8.8 and 10.0 us, the plan's two kernels and the gather 11.7, 17.4 and 19.2.
 struct SmallDispatch {
     QuantArgs q;  // the token rows, codes and permuted rows
     const int32_t *topk_idx;
@@ -480,7 +480,7 @@ cudaError_t launch_dispatch_int8(const void *x, const int32_t *topk_idx, int T, 
     q.q = x_q; q.scale = x_q_scale;
     q.inv_perm = inv_perm; q.K = K; q.n_perm = (int64_t)T * K;
     q.q_perm = x_perm_q; q.scale_perm = x_scale;
-    if (dispatch_int8_in_one(T, K)) {
+    if (dispatch_int8_in_one(T)) {
         SmallDispatch a{q, topk_idx, T, E, G, counts, offsets, send, send_tok, perm_token, inv_perm,
                         status};
         // Beside the 192 bytes that the kernel declares, 48 KB need no leave.  It is

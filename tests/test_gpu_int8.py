@@ -627,3 +627,22 @@ def test_operands_that_another_stream_writes(T, captured):
         assert torch.equal(q, want[3]) and torch.equal(s, want[4])
     for wsp in ws:
         assert moe.moe_read_device_status(wsp) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T,E,G,K,M", [(129, 64, 1, 32, 1), (192, 256, 8, 24, 8), (256, 256, 8, 32, 8),
+                                       (256, 40, 1, 17, 1), (256, 32, 1, 32, 1)])
+def test_dispatch_int8_of_one_block_and_many_copies(T, E, G, K, M):
+    """Batches of one launch with more than 4096 copies: up to 8192, every expert of a token's."""
+    cfg, g = config(T, 320, E, K, 64, G=G, M=M), gen(T + K)
+    x, idx = torch.randn(T, 320, device=DEV, generator=g).bfloat16(), routing(T, E, K, g, 0.6)
+    ws = moe.alloc_workspace(cfg)
+    before = moe.moe_launch_count()
+    o, q, s = dispatch(cfg, x, idx, ws)
+    assert moe.moe_launch_count() - before == 1
+    assert moe.moe_read_device_status(ws) == moe.MOE_OK
+    plain = {k: torch.empty_like(v) for k, v in o.items()}
+    moe.moe_dispatch(cfg, None, idx, *plain.values(), None, ws)
+    assert all(torch.equal(o[k], plain[k]) for k in o)
+    rq, rs = R.quantize(x.float())
+    tok = o["perm_token"].long()
+    assert torch.equal(q.double(), rq[tok]) and torch.equal(s.double(), rs[tok, 0])
