@@ -19,7 +19,7 @@
 //   r(s) = 1 - s, or (1 - e^(-s^2)) / (2 s^2) (1/2 at s = 0)
 // Both are one pass over the affinities.  The loss of 262144 tokens x 256 experts
 // takes 49 us and 2 for the sequences that cross tiles, 5.6 TB/s of its 277 MB:
-// HBM bounds it.  The gradient of 131072 x 256 takes 53 us, 5.1 TB/s of 268 MB; of
+// HBM bounds it.  The gradient of 131072 x 256 takes 51 us, 5.2 TB/s of 268 MB; of
 // 196601 x 64 with sqrt(softplus) 36 us, 2.8 TB/s, where the arithmetic of a value
 // (some 25 instructions) bounds it.  Short batches are bound by launch latency.
 //
@@ -378,8 +378,8 @@ __device__ __forceinline__ float softplus_ratio(float s) {
     return x < 0.25f ? y : __fdividef(0.5f - 0.5f * __expf(-x), x);
 }
 
-// Blocks an SM (four cost spills where a lane holds 16 values: 131072 x 256 took 62 us
-// with four, 56 with three; 196601 x 64 with 8 values 40 and 43).
+// Blocks an SM (four cost spills where a lane holds 16 values: 131072 x 256 takes 54 us
+// with four, 51 with three; 196601 x 64 with 8 values 35.6 and 37.8).
 template <class R>
 __host__ __device__ constexpr int grad_blocks() {
     return R::kValues <= 8 ? 4 : R::kValues <= 16 ? 3 : 1;
@@ -614,8 +614,11 @@ route_backward_kernel(const RouteGradArgs a) {
 // Calls f with the row layout for E experts.  Four experts a load where E allows it,
 // and as few lanes a token as hold its row in at most 16 values each (32 from 513
 // experts): a warp's steps are then shared by more tokens.  The router gradient of
-// 8.4 M affinities with twice the lanes (and half the values), in us: E = 64 68 for
-// 38, 128 38 for 36, 256 37 for 35; at 512, half the lanes 46 for 36.
+// 8.4 M affinities with twice the lanes (and half the values), in us: E = 64 34.9 for
+// 17.4, 128 17.4 for 14.5, 256 17.0 for 14.5; at 512, half the lanes 16.4 for 14.5.
+// Other E go one expert a load: 32768 tokens of 62 experts 16.5 us for 6.9 at 64, of 254
+// 18.9 for 14.4 at 256; above 256 a lane holds 32 values and an SM one block, 258
+// experts 66 us where 300, four a load, take 22.
 template <class F>
 cudaError_t with_row(int E, F f) {
     if (E % 4 == 0) {

@@ -188,9 +188,9 @@ cudaError_t launch_combine_backward(const void *d_out, const void *y_perm,
     if (T == 0 || (!d_y_perm && !d_topk_w)) return cudaSuccess;
     const uint4 *g = static_cast<const uint4 *>(d_out), *y = static_cast<const uint4 *>(y_perm);
     uint4 *dy = static_cast<uint4 *>(d_y_perm);
-    // Eight warps a row and one, in us, by d and copies: 2048: 256 2.5 and 3.5, 512 3.4 and
-    // 3.6, 1024 4.9 and 3.7; 4096: 1024 5.7 and 6.9, 8192 38 and 28; 7168: 1024 7.2 and 12.6,
-    // 8192 47 and 50, 65536 363 and 325.  The crossing grows as d^2.
+    // Eight warps a row and one, in us, by d and copies: 2048: 256 2.2 and 3.2, 512 3.0 and
+    // 3.3, 1024 4.4 and 3.4; 4096: 1024 4.9 and 5.5, 8192 30 and 21; 7168: 1024 5.4 and 8.3,
+    // 8192 44 and 45, 65536 354 and 323.  The crossing grows as d^2.
     if (n_rows * 8192 <= (int64_t)d * d)
         run_combine_backward<8>(g, y, inv_perm, topk_w, d / 8, K, n_rows, dy, d_topk_w, st);
     else

@@ -558,9 +558,10 @@ cudaError_t launch(const Maps &maps, const Params &p, const FfnInt8Args &a, cuda
     // weights would be loaded twice and in smaller tiles, where the reduction is long (an
     // epilogue no longer runs beside the next tile's products) and where each pair gets
     // many tiles (they are coarser).  us without and with:
-    //   256 experts of 7168 x 2048, K = 8: 8192 tokens 4370 4140, 9216 5040 4430, 12288
-    //   5750 5140; 4096 2650 2690 and 16384 (512 an expert and more) 6530 6910
-    //   (64 of 2048 x 1408, 4096 tokens of 6: 380 434; 32 of 7168 x 2048, 1024 of 8: 445 500)
+    //   256 experts of 7168 x 2048, K = 8: 8192 tokens 4230 4040, 9216 4980 4370, 12288
+    //   5820 5250; in both products 4096 2400 2530 and 16384 (512 an expert and more) 6910
+    //   7600 (64 of 2048 x 1408, 4096 tokens of 6: 320 360; 32 of 7168 x 2048, 1024 of 8:
+    //   424 469)
     const int64_t rows = (int64_t)a.T * a.K, blocks = (p.n_out_r + channels<EPI>() - 1) / channels<EPI>();
     const bool wide = rows >= 192ll * a.E && rows <= 448ll * a.E && p.k_r >= 32 * BK &&
                       a.E * blocks >= 32ll * (sms / 2);

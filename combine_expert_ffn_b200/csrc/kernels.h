@@ -256,8 +256,8 @@ cudaError_t launch_bias_update(const int32_t *counts, int E, int T, int K, float
 // make BAL_CLUSTER such tiles at most, the blocks of one cluster.  A block takes the
 // sequences of its tile one after the other, some 1.5 us each: where they average half
 // a tile or less, a tile is one average sequence, down to 8 tokens (1000 x 256 with 32,
-// 128 and 512 sequences 25.6, 61 and 168 us without, 15, 18.4 and 25 with; twice the
-// average 17.9, 18.4, 25) and to T / 2048, at most 2304 tiles (a long sequence among short
+// 128 and 512 sequences 13.8, 46 and 184 us without, 9.0, 9.7 and 18.5 with; twice the
+// average 11.9, 12.2, 29.7) and to T / 2048, at most 2304 tiles (a long sequence among short
 // ones is joined by one block).  part and part_n ([tiles, 2, E] each) hold the tiles'
 // shares of the sequences that cross them.
 constexpr int BAL_CLUSTER = 8;
