@@ -217,7 +217,8 @@ MOE_API moe_status moe_bias_update(const moe_config *cfg, const int32_t *counts,
  *                              calls that may overlap on the GPU need one each
  * Sums are fp32 over a fixed order (no float atomics: equal inputs give equal
  * bits), the loss over experts fp64.  Ids outside [0, E) are not counted, and
- * offsets outside the rule above are clamped; both are flagged
+ * offsets outside the rule above are clamped (nothing out of bounds is touched, but
+ * the outputs of that call are then not defined); both are flagged
  * MOE_ERR_DEVICE_FAULT in the status word.  n_seq == 0 is a no-op; T == 0 writes
  * zeros.  cfg->router and cfg->payload are not consulted.
  */
